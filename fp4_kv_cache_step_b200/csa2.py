@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libcsa2_fp4.so")
 MODE_FULL, MODE_REINDEX, MODE_REUSE = 0, 1, 2
 _MODES = {"FULL": MODE_FULL, "REINDEX": MODE_REINDEX, "REUSE": MODE_REUSE}
 STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "DEVICE_INDEX",
-          5: "NONFINITE", 6: "TIMEOUT", 7: "WORKSPACE"}
+          5: "NONFINITE", 6: "TIMEOUT", 7: "WORKSPACE", 8: "NO_PAGES"}
 
 
 class Csa2Error(RuntimeError):
@@ -46,12 +46,36 @@ class LayerArgs(ctypes.Structure):
                 ("swa_n", ctypes.c_void_p), ("Tw", ctypes.c_int), ("W", ctypes.c_int)]
 
 
+class PagesStruct(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("table", ctypes.c_void_p), ("len", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("P", ctypes.c_int), ("page", ctypes.c_int),
+                ("D", ctypes.c_int), ("S", ctypes.c_int), ("M", ctypes.c_int)]
+
+
+class NormRopeArgs(ctypes.Structure):
+    _fields_ = [("D", ctypes.c_int), ("R", ctypes.c_int), ("rot_begin", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("inverse", ctypes.c_int),
+                ("rot_scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("turns", ctypes.c_void_p), ("T", ctypes.c_int), ("Hq", ctypes.c_int),
+                ("q_norm", ctypes.c_int), ("q_f32", ctypes.c_int), ("q", ctypes.c_void_p),
+                ("q_stride", ctypes.c_longlong), ("pos", ctypes.c_void_p),
+                ("q_weight", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("E", ctypes.c_int),
+                ("kv_norm", ctypes.c_int), ("kv_f32", ctypes.c_int), ("kv", ctypes.c_void_p),
+                ("kv_stride", ctypes.c_longlong), ("kv_pos", ctypes.c_void_p),
+                ("kv_weight", ctypes.c_void_p), ("seq", ctypes.c_void_p),
+                ("entry", ctypes.c_void_p), ("kv_out", ctypes.c_void_p)]
+
+
 EXPORTS = ("fp4_kv_pack", "fp4_kv_unpack", "csa2_index_score", "csa2_topk",
            "csa2_sparse_attn_workspace_bytes", "csa2_sparse_attn",
            "csa2_layer_step_workspace_bytes", "csa2_layer_step", "csa2_check_device_errors",
            "csa2_last_error", "csa2_sparse_attn_noalloc", "fp4_kv_pack_g16", "fp4_kv_unpack_g16",
            "fp4_kv_append_g16", "csa2_sparse_attn_g16", "csa2_block_pool_workspace_bytes",
-           "csa2_block_pool", "csa2_sparse_attn_swa")
+           "csa2_block_pool", "csa2_sparse_attn_swa", "fp4_kv_pages_resize",
+           "fp4_kv_pages_resize_workspace_bytes", "fp4_kv_pages_fork",
+           "fp4_kv_pages_fork_workspace_bytes", "fp4_kv_pages_compact",
+           "fp4_kv_pages_compact_workspace_bytes", "csa2_rope_turns", "csa2_qk_norm_rope",
+           "csa2_paged_attn", "csa2_paged_attn_workspace_bytes")
 
 _lib = None
 
@@ -87,13 +111,30 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                                   ctypes.POINTER(SharedState)]
     L.csa2_layer_step_workspace_bytes.restype = Z
     L.csa2_layer_step.argtypes = [ctypes.POINTER(LayerArgs), I, ctypes.POINTER(SharedState), P, Z, P]
+    G = ctypes.POINTER(PagesStruct)
+    L.fp4_kv_pages_resize.argtypes = [G, P, P, I, P, Z, P]
+    L.fp4_kv_pages_fork.argtypes = [G, P, P, I, P, Z, P]
+    L.fp4_kv_pages_compact.argtypes = [G, P, P, Z, P]
+    L.fp4_kv_pages_resize_workspace_bytes.argtypes = [G, I]
+    L.fp4_kv_pages_fork_workspace_bytes.argtypes = [G, I]
+    L.fp4_kv_pages_compact_workspace_bytes.argtypes = [G]
+    L.csa2_rope_turns.argtypes = [I, ctypes.c_double, I, ctypes.c_double, ctypes.c_double,
+                                  ctypes.c_double, ctypes.c_double, P]
+    L.csa2_qk_norm_rope.argtypes = [ctypes.POINTER(NormRopeArgs), G, P]
+    L.csa2_paged_attn.argtypes = [P, G, P, P, P, I, I, I, I, F, P, P, P, Z, P]
+    L.csa2_paged_attn_workspace_bytes.argtypes = [G, I, I, I, I]
+    for f in ("fp4_kv_pages_resize", "fp4_kv_pages_fork", "fp4_kv_pages_compact",
+              "csa2_paged_attn"):
+        getattr(L, f + "_workspace_bytes").restype = Z
     L.csa2_check_device_errors.argtypes = [P]
     L.csa2_last_error.argtypes = []
     L.csa2_last_error.restype = ctypes.c_char_p
     for f in ("fp4_kv_pack", "fp4_kv_unpack", "csa2_index_score", "csa2_topk", "csa2_sparse_attn",
               "csa2_layer_step", "csa2_check_device_errors", "csa2_sparse_attn_noalloc",
               "fp4_kv_pack_g16", "fp4_kv_unpack_g16", "fp4_kv_append_g16", "csa2_sparse_attn_g16",
-              "csa2_block_pool", "csa2_sparse_attn_swa"):
+              "csa2_block_pool", "csa2_sparse_attn_swa", "fp4_kv_pages_resize",
+              "fp4_kv_pages_fork", "fp4_kv_pages_compact", "csa2_rope_turns", "csa2_qk_norm_rope",
+              "csa2_paged_attn"):
         getattr(L, f).restype = I
     _lib = L
     return L
@@ -416,3 +457,260 @@ def layer_step_workspace_bytes(mode, args: LayerArgs, shared: Csa2Shared) -> int
     m = _MODES[mode] if isinstance(mode, str) else int(mode)
     st = shared.c_struct()
     return int(load().csa2_layer_step_workspace_bytes(ctypes.byref(args), m, ctypes.byref(st)))
+
+
+# ------------------------------------------------------------------- paged cache
+def _i32(t, name, n, device):
+    """A contiguous int32 CUDA tensor of n values on `device`: its pointer."""
+    if t.dtype != torch.int32:
+        raise TypeError("%s must be torch.int32, got %s" % (name, t.dtype))
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with %d values, got shape %s"
+                         % (name, n, tuple(t.shape)))
+    return _at(t, name, device)
+
+
+def _at(t, name, device):
+    if t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    return t.data_ptr()
+
+
+def _call(name, device, *args):
+    """The C call of that name on the current stream of `device`, with that
+    device current (a default stream belongs to the current device)."""
+    fn = getattr(load(), name)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc != 0:
+        _check(rc, name)
+
+
+def _scratch(workspace, need, device):
+    """(pointer, bytes) of the caller's workspace, or of a new one."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+class Fp4Pages:
+    """A paged FP4 cache (fp4_kv_pages in csa2.h) over the caller's tensors: rows
+    uint8 [P][page][D/2 + D/16], table int32 [S][M] (-1: no page), length int32
+    [S], refs int32 [P] (0: the page is free). Holds the tensors, nothing else."""
+
+    def __init__(self, rows: torch.Tensor, table: torch.Tensor, length: torch.Tensor,
+                 refs: torch.Tensor):
+        _want(rows, torch.uint8, "rows", 3)
+        _want(table, torch.int32, "table", 2)
+        _want(length, torch.int32, "length", 1)
+        _want(refs, torch.int32, "refs", 1)
+        P, page, rb = rows.shape
+        S, M = table.shape
+        if rb % 72 != 0:
+            raise ValueError("rows of %d bytes hold no multiple of 128 channels" % rb)
+        if length.shape[0] != S or refs.shape[0] != P:
+            raise ValueError("length and refs must have S=%d and P=%d values" % (S, P))
+        if not rows.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        for t, name in ((rows, "rows"), (table, "table"), (length, "length"), (refs, "refs")):
+            _at(t, name, rows.device)
+            if not t.is_contiguous():
+                raise ValueError("expected contiguous %s" % name)
+        self.rows, self.table, self.length, self.refs = rows, table, length, refs
+        self.P, self.page, self.D, self.S, self.M = P, page, rb // 72 * 128, S, M
+        self.device = rows.device
+        self._c = PagesStruct(rows.data_ptr(), table.data_ptr(), length.data_ptr(),
+                              refs.data_ptr(), P, page, self.D, S, M)
+        self.ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, P: int, page: int, D: int, S: int, M: int, device="cuda") -> "Fp4Pages":
+        """A cache of P free pages and S empty slots of up to M pages."""
+        return cls(torch.zeros((P, page, g16_row_bytes(D)), dtype=torch.uint8, device=device),
+                   torch.full((S, M), -1, dtype=torch.int32, device=device),
+                   torch.zeros(S, dtype=torch.int32, device=device),
+                   torch.zeros(P, dtype=torch.int32, device=device))
+
+
+def fp4_kv_pages_resize(pages: Fp4Pages, seq: torch.Tensor, new_len: torch.Tensor,
+                        workspace: Optional[torch.Tensor] = None) -> None:
+    """Slots seq int32 [n] get new_len int32 [n] entries: pages behind are given
+    back, free ones taken lowest first; a shared, partly filled last page that
+    grows is copied. Length 0 frees a slot."""
+    n = seq.numel()
+    a, b = _i32(seq, "seq", n, pages.device), _i32(new_len, "new_len", n, pages.device)
+    ws, p, size = _scratch(workspace, load().fp4_kv_pages_resize_workspace_bytes(pages.ref, n),
+                           pages.device)
+    _call("fp4_kv_pages_resize", pages.device, pages.ref, a, b, n, p, size)
+
+
+def fp4_kv_pages_fork(pages: Fp4Pages, src: torch.Tensor, dst: torch.Tensor,
+                      workspace: Optional[torch.Tensor] = None) -> None:
+    """Slot dst[i] becomes a copy of slot src[i] (int32 [n], at once): the pages
+    are shared, what dst[i] held is given back."""
+    n = src.numel()
+    a, b = _i32(src, "src", n, pages.device), _i32(dst, "dst", n, pages.device)
+    ws, p, size = _scratch(workspace, load().fp4_kv_pages_fork_workspace_bytes(pages.ref, n),
+                           pages.device)
+    _call("fp4_kv_pages_fork", pages.device, pages.ref, a, b, n, p, size)
+
+
+def fp4_kv_pages_compact(pages: Fp4Pages, used: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None) -> None:
+    """Move the U pages in use to the places [0, U); used int32 [1] receives U."""
+    u = None if used is None else _i32(used, "used", 1, pages.device)
+    ws, p, size = _scratch(workspace, load().fp4_kv_pages_compact_workspace_bytes(pages.ref),
+                           pages.device)
+    _call("fp4_kv_pages_compact", pages.device, pages.ref, u, p, size)
+
+
+# ------------------------------------------------------------------- norm, rotation, append
+_ROPE_SCALING = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def csa2_rope_turns(R: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                    context: float = 0.0, fast: float = 32.0, slow: float = 1.0,
+                    device="cuda") -> torch.Tensor:
+    """Rotation frequencies of R channels as int64 [R/2]: the turns per position of
+    each pair, times 2^64 (computed on the host, then copied to `device`)."""
+    if scaling not in _ROPE_SCALING:
+        raise ValueError("scaling must be one of %s" % ", ".join(_ROPE_SCALING))
+    turns = torch.empty(max(0, R) // 2, dtype=torch.int64)
+    _check(load().csa2_rope_turns(int(R), float(base), _ROPE_SCALING[scaling], float(factor),
+                                  float(context), float(fast), float(slow),
+                                  turns.data_ptr() if turns.numel() else None), "csa2_rope_turns")
+    return turns.to(device)
+
+
+_ROW_TYPES = (torch.bfloat16, torch.float32)
+
+
+def csa2_qk_norm_rope(turns: torch.Tensor, rot_begin: int, interleaved: bool = True,
+                      inverse: bool = False, rot_scale: float = 1.0, eps: float = 1e-6,
+                      q: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                      q_norm: bool = True, q_weight: Optional[torch.Tensor] = None,
+                      q_out: Optional[torch.Tensor] = None, kv: Optional[torch.Tensor] = None,
+                      kv_pos: Optional[torch.Tensor] = None, kv_norm: bool = True,
+                      kv_weight: Optional[torch.Tensor] = None, pages: Optional[Fp4Pages] = None,
+                      seq: Optional[torch.Tensor] = None, entry: Optional[torch.Tensor] = None,
+                      kv_out: Optional[torch.Tensor] = None):
+    """RMS norm and rotary embedding of queries q [T][Hq][D] (bf16 or float32,
+    heads contiguous, any token stride) -> q_out bf16, and of entries kv [E][D]
+    quantised into row entry[e] of slot seq[e] of `pages` (kv_out: the bf16 values
+    that the rows stand for, when given). Either part may be left out. Channels
+    [rot_begin, rot_begin + R) turn by pos (kv_pos) int32 times `turns` [R/2]."""
+    if q is None and kv is None:
+        raise ValueError("nothing to do: give q, kv or both")
+    device = (q if q is not None else kv).device
+    _want(turns, torch.int64, "turns", 1)
+    a = NormRopeArgs()
+    a.R, a.rot_begin = 2 * turns.shape[0], int(rot_begin)
+    a.interleaved, a.inverse = int(bool(interleaved)), int(bool(inverse))
+    a.rot_scale, a.eps = rot_scale, eps
+    if a.R:
+        if not turns.is_contiguous():
+            raise ValueError("expected contiguous turns")
+        a.turns = _at(turns, "turns", device)
+    if q is not None:
+        if q.dtype not in _ROW_TYPES:
+            raise TypeError("q must be bfloat16 or float32, got %s" % q.dtype)
+        if q.dim() != 3 or (q.numel() and (q.stride(2) != 1 or (q.shape[1] > 1 and
+                                                               q.stride(1) != q.shape[2]))):
+            raise ValueError("q must be [T][Hq][D] with contiguous heads, got shape %s strides %s"
+                             % (tuple(q.shape), q.stride()))
+        T, H, D = q.shape
+        if q_out is None:
+            q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=device)
+        _want(q_out, torch.bfloat16, "q_out", 3)
+        if q_out.shape != q.shape or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous and shaped as q")
+        if pos is None:
+            raise ValueError("q needs pos")
+        a.T, a.Hq, a.D, a.q_norm, a.q_f32 = T, H, D, int(bool(q_norm)), q.dtype == torch.float32
+        a.q, a.q_out = _at(q, "q", device), _at(q_out, "q_out", device)
+        a.q_stride = q.stride(0) if T > 1 else H * D
+        a.pos = _i32(pos, "pos", T, device)
+        if q_weight is not None:
+            a.q_weight = _weight(q_weight, "q_weight", D, device)
+    if kv is not None:
+        if kv.dtype not in _ROW_TYPES:
+            raise TypeError("kv must be bfloat16 or float32, got %s" % kv.dtype)
+        if kv.dim() != 2 or (kv.numel() and kv.stride(1) != 1):
+            raise ValueError("kv must be [E][D] with contiguous rows, got shape %s strides %s"
+                             % (tuple(kv.shape), kv.stride()))
+        E, D = kv.shape
+        if q is not None and D != a.D:
+            raise ValueError("q and kv must have as many channels, got %d and %d" % (a.D, D))
+        if pages is None or kv_pos is None or seq is None or entry is None:
+            raise ValueError("kv needs kv_pos, pages, seq and entry")
+        if pages.device != device:
+            raise ValueError("pages must be on %s, got %s" % (device, pages.device))
+        a.E, a.D, a.kv_norm, a.kv_f32 = E, D, int(bool(kv_norm)), kv.dtype == torch.float32
+        a.kv = _at(kv, "kv", device)
+        a.kv_stride = kv.stride(0) if E > 1 else D
+        a.kv_pos = _i32(kv_pos, "kv_pos", E, device)
+        a.seq, a.entry = _i32(seq, "seq", E, device), _i32(entry, "entry", E, device)
+        if kv_weight is not None:
+            a.kv_weight = _weight(kv_weight, "kv_weight", D, device)
+        if kv_out is not None:
+            _want(kv_out, torch.bfloat16, "kv_out", 2)
+            if kv_out.shape != kv.shape or not kv_out.is_contiguous():
+                raise ValueError("kv_out must be contiguous and shaped as kv")
+            a.kv_out = _at(kv_out, "kv_out", device)
+    if device.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    _call("csa2_qk_norm_rope", device, ctypes.byref(a), pages.ref if pages is not None else None)
+    return q_out, kv_out
+
+
+def _weight(t, name, D, device):
+    _want(t, torch.float32, name, 1)
+    if t.shape[0] != D or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with D=%d values" % (name, D))
+    return _at(t, name, device)
+
+
+def csa2_paged_attn(q: torch.Tensor, pages: Fp4Pages, softmax_scale: float,
+                    seq: Optional[torch.Tensor] = None, nvalid: Optional[torch.Tensor] = None,
+                    topk_idx: Optional[torch.Tensor] = None, want_lse: bool = True,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None):
+    """q bf16 [B][Tq][Hq][512] over slots seq int32 [B] (None: slot b) of a paged
+    cache: all of the first nvalid int32 [B][Tq] entries (None: the slot's length),
+    or those listed in topk_idx int32 [B][Tq][K] -> (out bf16, lse float32 or None)."""
+    _want(q, torch.bfloat16, "q", 4)
+    device = pages.device
+    B, Tq, H, D = q.shape
+    if D != pages.D:
+        raise ValueError("q has %d channels, the pages %d" % (D, pages.D))
+    if not q.is_contiguous():
+        raise ValueError("expected a contiguous q")
+    K = 0
+    if topk_idx is not None:
+        _want(topk_idx, torch.int32, "topk_idx", 3)
+        K = topk_idx.shape[2]
+        if K == 0:
+            raise ValueError("topk_idx must list at least one place")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be bfloat16, contiguous and shaped as q")
+    if want_lse and lse is None:
+        lse = torch.empty((B, Tq, H), dtype=torch.float32, device=device)
+    elif want_lse and (lse.dtype != torch.float32 or lse.shape != q.shape[:3]
+                       or not lse.is_contiguous()):
+        raise ValueError("lse must be float32, contiguous and [B][Tq][Hq]")
+    ws, p, size = _scratch(workspace,
+                           load().csa2_paged_attn_workspace_bytes(pages.ref, B, Tq, H, K), device)
+    _call("csa2_paged_attn", device, _at(q, "q", device), pages.ref,
+          None if seq is None else _i32(seq, "seq", B, device),
+          None if nvalid is None else _i32(nvalid, "nvalid", B * Tq, device),
+          None if topk_idx is None else _i32(topk_idx, "topk_idx", B * Tq * K, device),
+          B, Tq, H, K, float(softmax_scale), _at(out, "out", device),
+          _at(lse, "lse", device) if want_lse else None, p, size)
+    return out, (lse if want_lse else None)

@@ -58,8 +58,15 @@ class DeviceScope {
     if (e != cudaSuccess) return e;
     int dev = cur;
     if (s != nullptr && s != cudaStreamLegacy && s != cudaStreamPerThread) {
-      e = cudaStreamGetDevice(s, &dev);
+      // a capturing stream cannot be asked for its device (the question would
+      // end the capture): it is captured with its device current
+      cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+      e = cudaStreamIsCapturing(s, &capture);
       if (e != cudaSuccess) return e;
+      if (capture == cudaStreamCaptureStatusNone) {
+        e = cudaStreamGetDevice(s, &dev);
+        if (e != cudaSuccess) return e;
+      }
     }
     if (dev != cur) {
       e = cudaSetDevice(dev);
@@ -150,6 +157,29 @@ cudaError_t launch_sparse_attn(const uint16_t* q, const uint8_t* kv_packed,
                                int Hq, int N, int K, float softmax_scale, uint16_t* out,
                                float* lse, void* workspace, int* err, cudaStream_t stream,
                                const SwaWindow* swa = nullptr, bool q_ready = false);
+
+// The paged cache (pages.cu); see fp4_kv_pages_resize, _fork, _compact.
+size_t pages_resize_workspace_bytes(const fp4_kv_pages& pg, int n);
+size_t pages_fork_workspace_bytes(const fp4_kv_pages& pg, int n);
+size_t pages_compact_workspace_bytes(const fp4_kv_pages& pg);
+cudaError_t launch_pages_resize(const fp4_kv_pages& pg, const int32_t* seq, const int32_t* new_len,
+                                int n, void* workspace, int* err, cudaStream_t stream);
+cudaError_t launch_pages_fork(const fp4_kv_pages& pg, const int32_t* src, const int32_t* dst,
+                              int n, void* workspace, int* err, cudaStream_t stream);
+cudaError_t launch_pages_compact(const fp4_kv_pages& pg, int32_t* used, void* workspace, int* err,
+                                 cudaStream_t stream);
+
+// Norm, rotary embedding and FP4 append (norm_rope.cu); see csa2_qk_norm_rope.
+cudaError_t launch_qk_norm_rope(const csa2_norm_rope_args& a, const fp4_kv_pages* pages, int* err,
+                                cudaStream_t stream);
+
+// Attention over a paged cache (paged_attn.cu); see csa2_paged_attn. topk_idx
+// NULL: every visible entry.
+size_t paged_attn_workspace_bytes(const fp4_kv_pages& pg, int B, int Tq, int Hq, int K);
+cudaError_t launch_paged_attn(const uint16_t* q, const fp4_kv_pages& pg, const int32_t* seq,
+                              const int32_t* nvalid, const int32_t* topk_idx, int B, int Tq,
+                              int Hq, int K, float softmax_scale, uint16_t* out, float* lse,
+                              void* workspace, int* err, cudaStream_t stream);
 
 // Tensor-core attention kernel (attn_tc.cu). With nsplit > 1 the splits are
 // merged inside the kernel (thread-block clusters, *merged set to true) when

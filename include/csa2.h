@@ -69,7 +69,8 @@ typedef enum {
   CSA2_ERR_DEVICE_INDEX = 4,  /* device saw an index outside its range or an unsorted pool */
   CSA2_ERR_NONFINITE = 5,     /* device saw a NaN or infinity where a finite value is needed */
   CSA2_ERR_TIMEOUT = 6,       /* a bounded device wait ran out */
-  CSA2_ERR_WORKSPACE = 7      /* workspace pointer NULL or smaller than required */
+  CSA2_ERR_WORKSPACE = 7,     /* workspace pointer NULL or smaller than required */
+  CSA2_ERR_NO_PAGES = 8       /* device: a paged cache had too few free pages */
 } csa2_status;
 
 /* The three static per-layer modes ([N] "The Three Modes Full Reindex And
@@ -374,6 +375,201 @@ CSA2_API size_t csa2_layer_step_workspace_bytes(const csa2_layer_args* args, csa
 
 CSA2_API csa2_status csa2_layer_step(const csa2_layer_args* args, csa2_mode mode, csa2_shared_state* st,
                             void* workspace, size_t workspace_bytes, csa2_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The paged cache: entries of the 16-channel layout (fp4_kv_pack_g16) in pages
+ * that many sequences share, grow into and give back. (An interface addition
+ * of this library; the pages that describe the model do not speak of one.)
+ * The caller owns the five device buffers; the library keeps no state. A page
+ * with refs 0 is free; refs counts the table places that hold a page. A cache
+ * starts with table -1, len 0 and refs 0 throughout.
+ *   rows   uint8 [P][page][D/2 + D/16]
+ *   table  int32 [S][M]    the pages of each sequence slot, in order; -1 past
+ *                          the last, ceil(len / page) of them
+ *   len    int32 [S]       entries of each slot
+ *   refs   int32 [P]
+ * Requires page a power of two in [8, 65536], D % 128 == 0, D <= 1024,
+ * 1 <= S <= 65536, M >= 1, P >= 1, M * page and P * page below 2^31, and every
+ * pointer 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  uint8_t* rows;
+  int32_t* table;
+  int32_t* len;
+  int32_t* refs;
+  int P, page, D, S, M;
+} fp4_kv_pages;
+
+/* ------------------------------------------------------------------------
+ * fp4_kv_pages_resize -- give n sequences new lengths. Shrinking gives back the
+ * pages behind the new length (length 0 frees the sequence). Growing takes free
+ * pages, lowest first, for the listed sequences in order; where a growing
+ * sequence's last page is partly filled and shared, its filled rows are copied
+ * to a new page first, so that what is appended stays its own. The rows of new
+ * entries are not written.
+ *   seq      int32 [n]   slots, each at most once
+ *   new_len  int32 [n]   in [0, M * page]
+ * Pages that the call gives back can be taken by later calls, not by this one.
+ * A slot outside [0, S) or listed twice, and a length outside its range, are
+ * recorded (CSA2_ERR_DEVICE_INDEX) and left as they are (all places of a slot
+ * listed twice). When the free pages run out, the sequences whose pages no
+ * longer fit are left as they are and CSA2_ERR_NO_PAGES is recorded; the ones
+ * that need no page are still resized.
+ *   workspace  fp4_kv_pages_resize_workspace_bytes(pages, n) bytes
+ * ------------------------------------------------------------------------ */
+CSA2_API size_t fp4_kv_pages_resize_workspace_bytes(const fp4_kv_pages* pages, int n);
+CSA2_API csa2_status fp4_kv_pages_resize(const fp4_kv_pages* pages, const int32_t* seq,
+                                         const int32_t* new_len, int n, void* workspace,
+                                         size_t workspace_bytes, csa2_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp4_kv_pages_fork -- make slot dst[i] a copy of slot src[i], for i < n at once:
+ * every source is read as it was before the call (so slots may be permuted),
+ * the pages that dst[i] held are given back and those of src[i] are shared. No
+ * row is copied: fp4_kv_pages_resize does that when a shared page is grown into.
+ *   src, dst   int32 [n]   a source may be listed often, a destination once
+ * A pair with a slot outside [0, S), and every pair of a destination listed
+ * twice, is recorded (CSA2_ERR_DEVICE_INDEX) and skipped.
+ *   workspace  fp4_kv_pages_fork_workspace_bytes(pages, n) bytes
+ * ------------------------------------------------------------------------ */
+CSA2_API size_t fp4_kv_pages_fork_workspace_bytes(const fp4_kv_pages* pages, int n);
+CSA2_API csa2_status fp4_kv_pages_fork(const fp4_kv_pages* pages, const int32_t* src,
+                                       const int32_t* dst, int n, void* workspace,
+                                       size_t workspace_bytes, csa2_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp4_kv_pages_compact -- move the pages in use to the places [0, U), U their
+ * number: the used pages at U and above go, in ascending order, to the free
+ * places below U, and the tables follow. The rows of the places left behind
+ * stay as they were.
+ *   used       int32 [1]   U; NULL to skip
+ *   workspace  fp4_kv_pages_compact_workspace_bytes(pages) bytes
+ * A table entry at U or above that names a free page is recorded
+ * (CSA2_ERR_DEVICE_INDEX) and becomes -1.
+ * ------------------------------------------------------------------------ */
+CSA2_API size_t fp4_kv_pages_compact_workspace_bytes(const fp4_kv_pages* pages);
+CSA2_API csa2_status fp4_kv_pages_compact(const fp4_kv_pages* pages, int32_t* used,
+                                          void* workspace, size_t workspace_bytes,
+                                          csa2_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * csa2_rope_turns -- the rotation frequencies of csa2_qk_norm_rope, computed on
+ * the HOST: turns[i] = round(2^64 * theta_i / (2 pi)), the turns of channel pair
+ * i per position as a binary fraction, so that position * turns[i] modulo 2^64 is
+ * the exact fraction of a turn at any position. theta_i = base^(-2 i / R), then
+ *   CSA2_ROPE_PLAIN   as it is
+ *   CSA2_ROPE_LINEAR  theta_i / factor (position interpolation)
+ *   CSA2_ROPE_NTK     base replaced by base * factor^(R / (R - 2))
+ *   CSA2_ROPE_YARN    (1 - g) theta_i / factor + g theta_i with
+ *                     g = clamp((r - slow) / (fast - slow), 0, 1) and
+ *                     r = context * theta_i / (2 pi), the turns of pair i over the
+ *                     context trained on (slow = 1 and fast = 32 are usual; the
+ *                     usual rot_scale is then 0.1 ln(factor) + 1)
+ *   turns    uint64 [R/2]   HOST memory, written
+ * Requires R even in [0, 1024], base > 1, factor >= 1, and for YARN context > 0
+ * and fast > slow.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+  CSA2_ROPE_PLAIN = 0,
+  CSA2_ROPE_LINEAR = 1,
+  CSA2_ROPE_NTK = 2,
+  CSA2_ROPE_YARN = 3
+} csa2_rope_scaling;
+
+CSA2_API csa2_status csa2_rope_turns(int R, double base, csa2_rope_scaling scaling, double factor,
+                                     double context, double fast, double slow, uint64_t* turns);
+
+/* ------------------------------------------------------------------------
+ * csa2_qk_norm_rope -- from projection outputs to queries and cache entries, in
+ * one launch: the RMS norm of each head (queries) and entry, the rotary
+ * embedding of the channels [rot_begin, rot_begin + R), and for entries the
+ * quantisation into their rows of a paged cache (entries are quantised after
+ * the rotary embedding, [N] "FP4 Main KV Cache To Halve Storage Again").
+ *   y = x * (mean(x^2) + eps)^(-1/2) * weight     (norm set; else y = x)
+ *   pairs (u, v) of y at position p, phi = 2 pi p turns[i] / 2^64:
+ *     (u, v) <- rot_scale (u cos phi - v sin phi, v cos phi + u sin phi)
+ *   with phi negated when `inverse` is set (an output of attention over rotated
+ *   entries is turned back this way: q = q_out = out, q_norm = 0). Pair i is
+ *   channels (2i, 2i + 1) of the rotary part when `interleaved`, else
+ *   (i, i + R/2).
+ * Queries (T > 0): computed in fp32, written as bf16.
+ *   q         [T][Hq][D]    bf16 (q_f32 0) or float (1); tokens q_stride
+ *                           elements apart, the heads of a token contiguous
+ *   pos       int32 [T]     positions, in [0, 2^31)
+ *   q_weight  float [D]     NULL for ones; ignored without q_norm
+ *   q_out     bf16 [T][Hq][D]   may be q itself (bf16, q_stride Hq * D)
+ * Entries (E > 0): computed in fp64 (a value next to a border of the E2M1 grid
+ * then falls to the side that the exact value lies on), scales and codes by
+ * the rule of fp4_kv_pack_g16. Entry e is entry `entry[e]` of slot `seq[e]`, whose
+ * page must be in the table and no other's (refs 1); an entry for which that
+ * does not hold is skipped and recorded (CSA2_ERR_DEVICE_INDEX). No row may be
+ * named twice.
+ *   kv        [E][D]        bf16 (kv_f32 0) or float (1), rows kv_stride
+ *                           elements apart
+ *   kv_pos, seq, entry  int32 [E]
+ *   kv_weight float [D]     NULL for ones; ignored without kv_norm
+ *   kv_out    bf16 [E][D]   optional (NULL to skip): the values that the row
+ *                           stands for (exact in bf16), also of a skipped entry
+ * A negative position is recorded (CSA2_ERR_DEVICE_INDEX) and turned the other way.
+ * A NaN or infinity in kv, after its norm and rotation, is recorded
+ * (CSA2_ERR_NONFINITE; the row is still written); in q it is passed on.
+ * Requires D % 128 == 0, D <= 1024 (pages->D == D), R even, 0 <= rot_begin,
+ * rot_begin + R <= D; data pointers 16-byte aligned and strides a multiple of 8
+ * elements (float: 4); pos, kv_pos, seq and entry 4-byte aligned; rows of the
+ * inputs no larger than their strides.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int D, R, rot_begin, interleaved, inverse;
+  float rot_scale, eps;
+  const uint64_t* turns;      /* [R/2], from csa2_rope_turns; NULL when R == 0 */
+  int T, Hq, q_norm, q_f32;
+  const void* q;
+  long long q_stride;
+  const int32_t* pos;
+  const float* q_weight;
+  uint16_t* q_out;
+  int E, kv_norm, kv_f32;
+  const void* kv;
+  long long kv_stride;
+  const int32_t* kv_pos;
+  const float* kv_weight;
+  const int32_t* seq;
+  const int32_t* entry;
+  uint16_t* kv_out;
+} csa2_norm_rope_args;
+
+CSA2_API csa2_status csa2_qk_norm_rope(const csa2_norm_rope_args* args, const fp4_kv_pages* pages,
+                                       csa2_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * csa2_paged_attn -- csa2_sparse_attn_g16 over a paged cache: the same softmax
+ * attention of q[b][t][h] over entries of slot seq[b], either all visible ones
+ * (topk_idx NULL; a context no longer than the top-K needs no indexer) or the
+ * listed ones.
+ *   q        uint16 [B][Tq][Hq][D]  bf16
+ *   seq      int32 [B]       slots; NULL: row b reads slot b (B <= S)
+ *   nvalid   int32 [B][Tq]   entries [0, nvalid) are visible; NULL: the slot's
+ *                            length. One outside [0, len] is recorded
+ *                            (CSA2_ERR_DEVICE_INDEX) and clamped to it
+ *   topk_idx int32 [B][Tq][K]   ids in [-1, nvalid), -1 skipped, others
+ *                            recorded and skipped; NULL (K ignored) for all
+ *   out      uint16 [B][Tq][Hq][D]  bf16
+ *   lse      float  [B][Tq][Hq]     optional, natural log; no entry gives
+ *                            out = 0 and lse = -inf
+ *   workspace  csa2_paged_attn_workspace_bytes() bytes (K 0 without topk_idx);
+ *              not shared by calls that may overlap
+ * A slot outside [0, S) is recorded and has no entries, and neither has a table
+ * place that holds no page. Requires pages->D == 512, 1 <= Hq, Tq >= 0,
+ * Tq * Hq <= 65535, B <= 65535.
+ * ------------------------------------------------------------------------ */
+CSA2_API size_t csa2_paged_attn_workspace_bytes(const fp4_kv_pages* pages, int B, int Tq, int Hq,
+                                                int K);
+CSA2_API csa2_status csa2_paged_attn(const uint16_t* q, const fp4_kv_pages* pages,
+                                     const int32_t* seq, const int32_t* nvalid,
+                                     const int32_t* topk_idx, int B, int Tq, int Hq, int K,
+                                     float softmax_scale, uint16_t* out, float* lse,
+                                     void* workspace, size_t workspace_bytes,
+                                     csa2_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Errors.
