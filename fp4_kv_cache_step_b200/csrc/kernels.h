@@ -181,6 +181,13 @@ cudaError_t launch_paged_attn(const uint16_t* q, const fp4_kv_pages& pg, const i
                               int Hq, int K, float softmax_scale, uint16_t* out, float* lse,
                               void* workspace, int* err, cudaStream_t stream);
 
+// Its kernel over every visible entry (paged_attn_tc.cu).
+size_t paged_attn_dense_workspace_bytes(const fp4_kv_pages& pg, int B, int Tq, int Hq);
+cudaError_t launch_paged_attn_dense(const uint16_t* q, const fp4_kv_pages& pg, const int32_t* seq,
+                                    const int32_t* nvalid, int B, int Tq, int Hq,
+                                    float softmax_scale, uint16_t* out, float* lse,
+                                    void* workspace, int* err, cudaStream_t stream);
+
 // Tensor-core attention kernel (attn_tc.cu). With nsplit > 1 the splits are
 // merged inside the kernel (thread-block clusters, *merged set to true) when
 // `merged` is non-null and the cluster fits; otherwise partials go to

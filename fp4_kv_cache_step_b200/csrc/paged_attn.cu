@@ -1,8 +1,8 @@
-// paged_attn.cu -- attention over the paged FP4 cache (csa2_paged_attn).
-//
-// The entries of each query row are listed as rows of the whole pool (one
-// physical row number per entry: page * table place + offset), and the attention
-// over the 16-channel layout runs over that list with the pool as one sequence.
+// paged_attn.cu -- attention over the paged FP4 cache (csa2_paged_attn). Without
+// a list the kernel of paged_attn_tc.cu walks the pages. With one, the listed
+// entries become rows of the whole pool (page from the table * page size +
+// offset), and the attention over the 16-channel layout runs over that list with
+// the pool as one sequence.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -25,7 +25,7 @@ __device__ __forceinline__ int visible(const fp4_kv_pages& pg, int s, const int3
   return min(max(0, n), len);
 }
 
-// list[row][i] = the pool row of entry ids[row][i] (ids NULL: entry i), or -1.
+// list[row][i] = the pool row of entry ids[row][i], or -1.
 __global__ void __launch_bounds__(kThreads)
 list_rows_kernel(const fp4_kv_pages pg, int shift, const int32_t* __restrict__ seq,
                  const int32_t* __restrict__ nvalid, const int32_t* __restrict__ ids, int Tq, int K,
@@ -36,7 +36,7 @@ list_rows_kernel(const fp4_kv_pages pg, int shift, const int32_t* __restrict__ s
   const int s = seq ? seq[b] : b;
   const int n = visible(pg, s, nvalid, row, err);
   for (int i = blockIdx.y * kThreads + threadIdx.x; i < K; i += gridDim.y * kThreads) {
-    int e = ids ? ids[row * K + i] : (i < n ? i : -1);
+    const int e = ids[row * K + i];
     int at = -1;
     if (e < -1 || e >= n) {
       record_error(err, CSA2_ERR_DEVICE_INDEX);
@@ -56,7 +56,7 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
 size_t paged_attn_workspace_bytes(const fp4_kv_pages& pg, int B, int Tq, int Hq, int K) {
-  if (K == 0) K = pg.M * pg.page;
+  if (K == 0) return paged_attn_dense_workspace_bytes(pg, B, Tq, Hq);
   return up256((size_t)B * Tq * K * 4) + sparse_attn_workspace_bytes(1, B * Tq, Hq, K);
 }
 
@@ -65,7 +65,9 @@ cudaError_t launch_paged_attn(const uint16_t* q, const fp4_kv_pages& pg, const i
                               int Hq, int K, float softmax_scale, uint16_t* out, float* lse,
                               void* workspace, int* err, cudaStream_t stream) {
   if (B == 0 || Tq == 0) return cudaSuccess;
-  if (topk_idx == nullptr) K = pg.M * pg.page;
+  if (topk_idx == nullptr)
+    return launch_paged_attn_dense(q, pg, seq, nvalid, B, Tq, Hq, softmax_scale, out, lse,
+                                   workspace, err, stream);
   int shift = 0;
   while ((1 << shift) < pg.page) ++shift;
   int32_t* list = static_cast<int32_t*>(workspace);
