@@ -44,26 +44,28 @@ using namespace sm100;
 
 constexpr int kD = kHeadDim;               // 512
 constexpr int kRows = 64;                  // query rows of a block
-constexpr int kT = 96;                     // entries of a tile
-constexpr int kAtom = kT * 128;            // 96 entries x 64 channels of fp16
+constexpr int kT = 80;                     // entries of a tile
+constexpr int kHalfT = kT / 2;
+constexpr int kAtom = kT * 128;            // 80 entries x 64 channels of fp16
 constexpr int kVTile = 8 * kAtom;
-constexpr int kPTile = 2 * 8192;           // 64 rows x (64 + 32) entries of fp16, 128-byte rows
+constexpr int kPTile = 2 * 8192;           // 64 rows x (64 + 16) entries of fp16, 128-byte rows
+constexpr int kRowBytes = kD / 2 + kD / 16;     // 288
+constexpr int kRawTile = kT * kRowBytes;
 constexpr int kProducerWarps = 8;
-constexpr int kPerWarp = kT / kProducerWarps;   // 12 entries of a tile per producer warp
+constexpr int kPerWarp = kT / kProducerWarps;   // 10 entries of a tile per producer warp
 constexpr int kMmaWarp = 8;
-constexpr int kThreads = 13 * 32;
+constexpr int kLoadWarp = 13;
+constexpr int kThreads = 14 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemQ = 256, kTmemS = 384;
 constexpr uint32_t kHalfLanes = 16u << 16;      // lanes 16-31 of a quadrant
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleSlack = 8.0f;
-constexpr int kRowBytes = kD / 2 + kD / 16;     // 288
-constexpr uint32_t kAllValid = (1u << (2 * kPerWarp)) - 1u;   // two warps' entries
 
 struct __align__(8) Bars {
   uint64_t q_ld, q_conv, q_full, q_free, o_full, s_full, s_free;
-  uint64_t v_full[2], v_free[2], p_full[2];
+  uint64_t raw_full[2], raw_free[2], v_full[2], v_free[2], p_full;
 };
 
 struct Smem {
@@ -73,14 +75,13 @@ struct Smem {
   long long base;                   // tiles before the first sequence of this piece
   long long total;                  // tiles in all
   int first_b;
-  int pad;
-  uint16_t valid[2][kProducerWarps];   // bit i: entry i of the warp's 12 is there
+  uint32_t valid[4][3];             // bit i of a tile's 96: entry i is there
   float2 mlf[kRows];                // (reference maximum, row sum)
   float factor[kRows];              // rescaling of each row
   float qdown[kRows];               // the power of two each row was scaled up by, inverted
 };
 
-constexpr size_t kSmemBytes = 1024 + 2 * kVTile + 2 * kPTile + sizeof(Smem);
+constexpr size_t kSmemBytes = 1024 + 2 * kVTile + kPTile + 2 * kRawTile + sizeof(Smem);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 
 struct Params {
@@ -135,6 +136,15 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
+// One lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)::"memory");
+  return r != 0;
+}
+
 __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
@@ -165,15 +175,14 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// loads that stay in program order among the other volatile asm
-__device__ __forceinline__ uint2 ldg_v2(const void* ptr) {
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 r;
-  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(ptr));
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
   return r;
 }
-__device__ __forceinline__ uint32_t ldg_u8(const void* ptr) {
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
   uint32_t r;
-  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(r) : "l"(ptr));
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
   return r;
 }
 
@@ -196,26 +205,69 @@ __device__ __forceinline__ uint4 dq8(uint32_t codes, __half2 scale) {
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-// The sum of 16 columns of the two partial logits of a row: threads 0-15 read
-// columns taddr .. + 15, threads 16-31 columns taddr + 48 .. + 63, of lanes
-// 0-15 and 16-31 of the quadrant.
+// The sum of 8 columns of the two partial logits of a row: threads 0-15 read
+// columns taddr .. + 7, threads 16-31 columns taddr + 40 .. + 47, of lanes 0-15
+// and 16-31 of the quadrant.
 __device__ __forceinline__ void tmem_ld_partials(uint32_t taddr, float* y) {
+  uint32_t a[8], b[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16], %18;\n\t"
+      "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17], %18;\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
+        "=r"(a[7]), "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]),
+        "=r"(b[6]), "=r"(b[7])
+      : "r"(taddr), "r"(taddr + kHalfLanes), "n"(kHalfT)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
+}
+__device__ __forceinline__ void tmem_ld_partials16(uint32_t taddr, float* y) {
   uint32_t a[16], b[16];
   asm volatile(
       "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32], 48;\n\t"
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32], %34;\n\t"
       "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
-      "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33], 48;\n\t"
+      "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33], %34;\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
         "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]),
         "=r"(a[14]), "=r"(a[15]), "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]),
         "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]),
         "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
-      : "r"(taddr), "r"(taddr + kHalfLanes)
+      : "r"(taddr), "r"(taddr + kHalfLanes), "n"(kHalfT)
       : "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
+}
+
+// mbar_wait without its sleeps: the hardware suspends the thread in try_wait
+// (up to a microsecond at a time), and wakes it with the phase
+__device__ __forceinline__ bool wait_hot(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((it & 63u) == 63u) {
+      if (t0 == 0) t0 = global_ns();
+      if (*abort) return false;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool wait_hot_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const bool ok = wait_hot(bar, parity, abort);
+  return __all_sync(0xffffffffu, ok) != 0;
 }
 
 // Whether any of the softmax threads says so (also a barrier among them).
@@ -268,11 +320,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* vs = base;                          // [2][8 atoms][96 entries][128 B]
-  uint8_t* ps = vs + 2 * kVTile;               // [2][2 atoms][64 rows][128 B]
-  Smem& sm = *reinterpret_cast<Smem*>(ps + 2 * kPTile);
+  uint8_t* vs = base;                          // [2][8 atoms][80 entries][128 B]
+  uint8_t* ps = vs + 2 * kVTile;               // [2 atoms][64 rows][128 B]
+  uint8_t* raw = ps + kPTile;                  // [2][80 entries][288 B]
+  Smem& sm = *reinterpret_cast<Smem*>(raw + 2 * kRawTile);
   volatile int* abort_flag = &sm.abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     mbar_init(&sm.bar.q_ld, 1);
@@ -285,8 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.bar.v_full[i], kProducerWarps);
       mbar_init(&sm.bar.v_free[i], 1);
-      mbar_init(&sm.bar.p_full[i], 4);
+      mbar_init(&sm.bar.raw_full[i], 1);
+      mbar_init(&sm.bar.raw_free[i], kProducerWarps);
     }
+    mbar_init(&sm.bar.p_full, 4);
     sm.abort_flag = 0;
     fence_mbar_init();
   }
@@ -383,44 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
     if (warp < kProducerWarps) {
       // ---------------------------------------------------------- load + dequantise
       // Lane 16 j + u takes channels 16u .. + 15 and 256 + 16u .. + 15 of entries
-      // 12 w + 2 r + j of a tile, r = 0 .. 5: each load of a warp covers whole
-      // lines of two rows.
+      // 10 w + 2 r + j of a tile, r = 0 .. 4: whole lines of two rows at a time.
       const int u = lane & 15, half = lane >> 4;
-      const int s = p.seq ? __ldg(p.seq + b) : b;
-      const int32_t* table = p.pg.table + (size_t)(n_most > 0 ? s : 0) * p.pg.M;
-      // lanes 0-11: the table place of entry 12 w + lane of tile t (checked a
-      // tile later, when the load has landed), -2 past the visible entries
-      auto fetch = [&](int t) -> int {
-        const int e = (t0 + t) * kT + warp * kPerWarp + lane;
-        return lane < kPerWarp && t < nt && e < n_most ? __ldg(table + (e >> p.shift)) : -2;
-      };
-      auto to_row = [&](int place, int t) -> int {
-        if (place == -2) return -1;
-        if (place < 0 || place >= p.pg.P) {
-          record_error(p.err, CSA2_ERR_DEVICE_INDEX);
-          return -1;
-        }
-        const int e = (t0 + t) * kT + warp * kPerWarp + lane;
-        return (place << p.shift) + (e & (p.pg.page - 1));
-      };
-      struct Raw {
-        uint2 c0, c1;
-        uint32_t s0, s1;
-      };
-      Raw raw[kPerWarp / 2];
-      auto load = [&](int rows, int r) {
-        const int id = __shfl_sync(0xffffffffu, rows, 2 * r + half);
-        if (id >= 0) {
-          const uint8_t* pr = p.pg.rows + (size_t)id * kRowBytes;
-          raw[r].c0 = ldg_v2(pr + 8 * u);
-          raw[r].c1 = ldg_v2(pr + 128 + 8 * u);
-          raw[r].s0 = ldg_u8(pr + 256 + u);
-          raw[r].s1 = ldg_u8(pr + 272 + u);
-        } else {
-          raw[r].c0 = raw[r].c1 = make_uint2(0, 0);
-          raw[r].s0 = raw[r].s1 = 0;
-        }
-      };
       // the query block: see sparse attention's staging; rows are converted in
       // place to fp16, scaled by a power of two per row (exact), then moved to
       // tensor memory, thread (row, channel half) of two warps per quadrant
@@ -498,114 +518,188 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
         }
       };
 
-      int rows_next = to_row(fetch(0), 0);
-      int place_after = fetch(1);
-#pragma unroll
-      for (int r = 0; r < kPerWarp / 2; ++r) load(rows_next, r);
       stage_q();
       for (int t = 0; t < nt; ++t) {
         const uint32_t g = g0 + t;
         const int buf = (int)(g & 1);
-        const uint32_t vb = __ballot_sync(0xffffffffu, rows_next >= 0);
-        rows_next = to_row(place_after, t + 1);
-        place_after = fetch(t + 2);
-        if (!mbar_wait_warp(&sm.bar.v_free[buf], ((g >> 1) & 1) ^ 1, abort_flag)) break;
-        if (t == 1 && !mbar_wait_warp(&sm.bar.q_free, sph, abort_flag)) break;
-        if (lane == 0) sm.valid[buf][warp] = (uint16_t)vb;
+        const uint32_t ph = (g >> 1) & 1;
+        if (!wait_hot_warp(&sm.bar.raw_full[buf], ph, abort_flag)) break;
+        if (!wait_hot_warp(&sm.bar.v_free[buf], ph ^ 1, abort_flag)) break;
+        if (t == 1 && !wait_hot_warp(&sm.bar.q_free, sph, abort_flag)) break;
         const uint32_t tile = vs_s + (uint32_t)(buf * kVTile);
+        const uint32_t rows = smem_u32(raw) + (uint32_t)(buf * kRawTile);
+        const uint32_t* valid = sm.valid[g & 3];
 #pragma unroll
         for (int r = 0; r < kPerWarp / 2; ++r) {
           const int e = warp * kPerWarp + 2 * r + half;
-          const __half2 f0 = e4m3x2_to_half2((uint16_t)(raw[r].s0 * 0x0101u));
-          const __half2 f1 = e4m3x2_to_half2((uint16_t)(raw[r].s1 * 0x0101u));
-          const uint4 d0 = dq8(raw[r].c0.x, f0), d1 = dq8(raw[r].c0.y, f0);
-          const uint4 d2 = dq8(raw[r].c1.x, f1), d3 = dq8(raw[r].c1.y, f1);
-          load(rows_next, r);
+          const uint32_t row = rows + (uint32_t)(e * kRowBytes);
+          uint2 c0 = lds64(row + 8 * u), c1 = lds64(row + 128 + 8 * u);
+          uint32_t s0 = lds8(row + 256 + u), s1 = lds8(row + 272 + u);
+          if (!(valid[e >> 5] >> (e & 31) & 1u)) {      // nothing was copied there
+            c0 = c1 = make_uint2(0, 0);
+            s0 = s1 = 0;
+          }
+          const __half2 f0 = e4m3x2_to_half2((uint16_t)(s0 * 0x0101u));
+          const __half2 f1 = e4m3x2_to_half2((uint16_t)(s1 * 0x0101u));
           // channels 256 hh + 16 u: atom 4 hh + u / 4, 16-byte chunks 2 (u % 4), + 1
           const uint32_t a0 = tile + (uint32_t)((u >> 2) * kAtom), a1 = a0 + 4u * kAtom;
-          const int c = (u & 3) * 2;
-          sts128(a0 + swz(e, c), d0);
-          sts128(a0 + swz(e, c + 1), d1);
-          sts128(a1 + swz(e, c), d2);
-          sts128(a1 + swz(e, c + 1), d3);
+          // lanes u and u + 4 would meet in one bank group: every other four take
+          // their two chunks in the other order
+          const int odd = (u >> 2) & 1, c = (u & 3) * 2 + odd;
+          sts128(a0 + swz(e, c), dq8(odd ? c0.y : c0.x, f0));
+          sts128(a0 + swz(e, c ^ 1), dq8(odd ? c0.x : c0.y, f0));
+          sts128(a1 + swz(e, c), dq8(odd ? c1.y : c1.x, f1));
+          sts128(a1 + swz(e, c ^ 1), dq8(odd ? c1.x : c1.y, f1));
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.bar.v_full[buf]);
+        if (lane == 0) {
+          mbar_arrive(&sm.bar.v_full[buf]);
+          mbar_arrive(&sm.bar.raw_free[buf]);
+        }
+      }
+    } else if (warp == kLoadWarp) {
+      // ---------------------------------------------------------- bulk copies
+      // Lane i copies the rows of a tile that lie in its i-th page (a tile of 80
+      // entries touches at most 11 pages of 8).
+      const int s = p.seq ? __ldg(p.seq + b) : b;
+      const int32_t* table = p.pg.table + (size_t)(n_most > 0 ? s : 0) * p.pg.M;
+      // entries [lo, hi) of the sequence in lane i's page of tile t
+      auto range = [&](int t, long long* lo, long long* hi) {
+        const long long e0 = (long long)(t0 + t) * kT;
+        const long long pg = (e0 >> p.shift) + lane;
+        *lo = max(e0, pg << p.shift);
+        *hi = max(*lo, min(min(e0 + kT, (long long)n_most), (pg + 1) << p.shift));
+        return pg;
+      };
+      auto fetch = [&](int t) -> int {
+        if (t >= nt) return -1;
+        long long lo, hi;
+        const long long pg = range(t, &lo, &hi);
+        return hi > lo ? __ldg(table + pg) : -1;
+      };
+      int place = fetch(0);
+      for (int t = 0; t < nt; ++t) {
+        const uint32_t g = g0 + t;
+        const int buf = (int)(g & 1);
+        long long lo, hi;
+        range(t, &lo, &hi);
+        const int place_next = fetch(t + 1);
+        if (hi > lo && (place < 0 || place >= p.pg.P)) {
+          record_error(p.err, CSA2_ERR_DEVICE_INDEX);
+          hi = lo;
+        }
+        const int count = (int)(hi - lo);
+        const int at = count ? (int)(lo - (long long)(t0 + t) * kT) : 0;   // place in the tile
+        uint32_t bits[3];
+#pragma unroll
+        for (int w = 0; w < 3; ++w) {
+          const int x0 = min(32, max(0, at - 32 * w)), x1 = min(32, max(0, at + count - 32 * w));
+          const uint32_t m = (x1 >= 32 ? ~0u : (1u << x1) - 1u) & ~(x0 >= 32 ? ~0u : (1u << x0) - 1u);
+          bits[w] = __reduce_or_sync(0xffffffffu, count ? m : 0u);
+        }
+        if (!wait_hot_warp(&sm.bar.raw_free[buf], ((g >> 1) & 1) ^ 1, abort_flag)) break;
+        if (lane == 0) {
+#pragma unroll
+          for (int w = 0; w < 3; ++w) sm.valid[g & 3][w] = bits[w];
+          mbar_arrive_expect_tx(&sm.bar.raw_full[buf],
+                                (uint32_t)(__popc(bits[0]) + __popc(bits[1]) + __popc(bits[2])) *
+                                    kRowBytes);
+        }
+        __syncwarp();
+        if (count)
+          bulk_load(raw + buf * kRawTile + at * kRowBytes,
+                    p.pg.rows + (((size_t)place << p.shift) + (size_t)(lo & (p.pg.page - 1))) * kRowBytes,
+                    (uint32_t)count * kRowBytes, &sm.bar.raw_full[buf]);
+        place = place_next;
       }
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        const uint32_t id_s = idesc_f16(64, kT, 0);
-        const uint32_t id_o = idesc_f16(128, kRows, 1);
-        const uint64_t vk = desc_sw128(vs_s, 16, 1024);       // V as K-major B
-        const uint64_t vm = desc_sw128(vs_s, kAtom, 1024);    // V as M-major A
-        const uint64_t pk = desc_sw128(ps_s, 16, 1024);       // P as K-major B
-        bool ok = mbar_wait(&sm.bar.q_full, sph, abort_flag);
+      // The whole warp runs this with warp-uniform values and one elected lane
+      // issues: descriptors then stay in uniform registers (from one divergent
+      // thread an instruction took 65 to 80 cycles to issue, more than to run).
+      const uint32_t id_s = idesc_f16(64, kT, 0);
+      const uint32_t id_o = idesc_f16(128, kRows, 1);
+      const uint64_t vk = desc_sw128(vs_s, 16, 1024);       // V as K-major B
+      const uint64_t vm = desc_sw128(vs_s, kAtom, 1024);    // V as M-major A
+      const uint64_t pk = desc_sw128(ps_s, 16, 1024);       // P as K-major B
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t gu = __shfl_sync(0xffffffffu, g0, 0);
+      const int ntu = __shfl_sync(0xffffffffu, nt, 0);
+      bool ok = wait_hot_warp(&sm.bar.q_full, sph, abort_flag);
+      tc_fence_after();
+      auto issue_s = [&](uint32_t buf) {
         tc_fence_after();
-        auto issue_s = [&](uint32_t g) {
-          tc_fence_after();
-          const uint64_t v = vk + (uint64_t)(((g & 1) * kVTile) >> 4);
+        const uint64_t v = vk + (uint64_t)((buf * kVTile) >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 16; ++k)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
-              mma_ts(tmem + hf * kHalfLanes + kTmemS, tmem + hf * kHalfLanes + kTmemQ + 8u * k,
+              mma_ts(tm + hf * kHalfLanes + kTmemS, tm + hf * kHalfLanes + kTmemQ + 8u * k,
                      v + (uint64_t)(((4 * hf + (k >> 2)) * kAtom + (k & 3) * 32) >> 4), id_s,
                      k > 0 ? 1u : 0u);
           mma_commit(&sm.bar.s_full);
-        };
-        auto issue_pv = [&](uint32_t g, bool first) {
-          tc_fence_after();
-          const uint64_t v = vm + (uint64_t)(((g & 1) * kVTile) >> 4);
-          const uint64_t pp = pk + (uint64_t)(((g & 1) * kPTile) >> 4);
+        }
+        __syncwarp();
+      };
+      auto issue_pv = [&](uint32_t buf, uint32_t acc0) {
+        tc_fence_after();
+        const uint64_t v = vm + (uint64_t)((buf * kVTile) >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int ks = 0; ks < kT / 16; ++ks)
-              mma_ss(tmem + 64u * j, v + (uint64_t)((2 * j * kAtom + ks * 2048) >> 4),
-                     pp + (uint64_t)(((ks >> 2) * 8192 + (ks & 3) * 32) >> 4), id_o,
-                     (ks > 0 || !first) ? 1u : 0u);
-          mma_commit(&sm.bar.v_free[g & 1]);
-        };
-        // whichever is ready first: S of a tile (filled, and the logits before
-        // it read) or O^T += of a tile (its P published)
-        int next_s = 0, next_pv = 0;
-        uint64_t t_last = 0;
-        uint32_t spins = 0;
-        while (ok && next_pv < nt) {
-          bool did = false;
-          const uint32_t gs = g0 + next_s, gp = g0 + next_pv;
-          if (next_s < nt && mbar_test_wait(&sm.bar.s_free, (gs & 1) ^ 1) &&
-              mbar_test_wait(&sm.bar.v_full[gs & 1], (gs >> 1) & 1)) {
-            issue_s(gs);
-            ++next_s;
-            did = true;
-          }
-          if (next_pv < next_s && mbar_test_wait(&sm.bar.p_full[gp & 1], (gp >> 1) & 1)) {
-            issue_pv(gp, next_pv == 0);
-            ++next_pv;
-            did = true;
-          }
-          if (did) {
-            spins = 0;
-          } else {
-            __nanosleep(20);
-            if ((++spins & 63u) == 0u) {
-              if (spins == 64u) t_last = global_ns();
-              if (*abort_flag || global_ns() - t_last > kWaitLimitNs) {
-                *abort_flag = 1;
-                ok = false;
-              }
+              mma_ss(tm + 64u * j, v + (uint64_t)((2 * j * kAtom + ks * 2048) >> 4),
+                     pk + (uint64_t)(((ks >> 2) * 8192 + (ks & 3) * 32) >> 4), id_o,
+                     ks > 0 ? 1u : acc0);
+          mma_commit(&sm.bar.v_free[buf]);
+        }
+        __syncwarp();
+      };
+      auto done = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) != 0;
+      };
+      // whichever is ready first: S of a tile (filled, and the logits before it
+      // read) or O^T += of a tile (its P published)
+      int next_s = 0, next_pv = 0;
+      uint64_t t_last = 0;
+      uint32_t spins = 0;
+      while (ok && next_pv < ntu) {
+        bool did = false;
+        const uint32_t gs = gu + next_s, gp = gu + next_pv;
+        if (next_s < ntu && done(&sm.bar.s_free, (gs & 1) ^ 1) &&
+            done(&sm.bar.v_full[gs & 1], (gs >> 1) & 1)) {
+          issue_s(gs & 1);
+          ++next_s;
+          did = true;
+        }
+        if (next_pv < next_s && done(&sm.bar.p_full, gp & 1)) {
+          issue_pv(gp & 1, next_pv > 0 ? 1u : 0u);
+          ++next_pv;
+          did = true;
+        }
+        if (did) {
+          spins = 0;
+        } else {
+          __nanosleep(20);
+          if ((++spins & 63u) == 0u) {
+            const uint64_t now = global_ns();
+            if (spins == 64u) t_last = now;
+            if (__any_sync(0xffffffffu, *abort_flag != 0 || now - t_last > kWaitLimitNs)) {
+              *abort_flag = 1;
+              ok = false;
             }
           }
         }
-        mma_commit(&sm.bar.o_full);
-        // nothing may be in flight when tensor memory is reused or released
-        mbar_wait(&sm.bar.o_full, sph, abort_flag);
       }
+      if (elect_one()) mma_commit(&sm.bar.o_full);
+      __syncwarp();
+      // nothing may be in flight when tensor memory is reused or released
+      wait_hot_warp(&sm.bar.o_full, sph, abort_flag);
     } else {
-      // ---------------------------------------------------------- softmax
+      // ---------------------------------------------------------- softmax (warps 9-12)
       const int hl = lane & 15, ch = lane >> 4;
       const int h = quad * 16 + hl;
       bool ok = mbar_wait_warp(&sm.bar.q_full, sph, abort_flag);
@@ -616,43 +710,42 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
       for (int t = 0; t < nt; ++t) {
         const uint32_t g = g0 + t;
         const int buf = (int)(g & 1);
-        // (S complete also means that O^T += of tile t - 2 is: its P buffer is free)
-        ok = ok && mbar_wait_warp(&sm.bar.v_full[buf], (g >> 1) & 1, abort_flag) &&
-             mbar_wait_warp(&sm.bar.s_full, g & 1, abort_flag);
+        ok = ok && wait_hot_warp(&sm.bar.v_full[buf], (g >> 1) & 1, abort_flag) &&
+             wait_hot_warp(&sm.bar.s_full, g & 1, abort_flag);
         // every softmax warp takes part in the barriers below, or none does
         if (softmax_any(!ok)) break;
         tc_fence_after();
-        // this thread's entries: 48 ch .. + 47 of the tile, two masks of 24
-        const int left = n_row - (t0 + t) * kT - 48 * ch;
+        // this thread's entries: 40 ch .. + 39 of the tile, masks of 32 and 8
+        const int left = n_row - (t0 + t) * kT - kHalfT * ch;
         uint32_t m0, m1;
         {
-          const uint2 v = *reinterpret_cast<const uint2*>(&sm.valid[buf][4 * ch]);
-          m0 = (v.x & 0xfffu) | ((v.x >> 16) << 12);
-          m1 = (v.y & 0xfffu) | ((v.y >> 16) << 12);
-          if (left < 48) {
-            m0 &= left <= 0 ? 0u : left >= 24 ? kAllValid : (1u << left) - 1u;
-            m1 &= left <= 24 ? 0u : (1u << (left - 24)) - 1u;
+          const uint32_t* v = sm.valid[g & 3];
+          m0 = ch ? (v[1] >> 8) | (v[2] << 24) : v[0];
+          m1 = (ch ? v[2] >> 8 : v[1]) & 0xffu;
+          if (left < kHalfT) {
+            m0 &= left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1u;
+            m1 &= left <= 32 ? 0u : (1u << (left - 32)) - 1u;
           }
         }
-        const bool all = __all_sync(0xffffffffu, (m0 & m1) == kAllValid);
-        float y[48];
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-          tmem_ld_partials(tmem + lanes + kTmemS + 16u * k, y + 16 * k);
+        const bool all = __all_sync(0xffffffffu, m0 == ~0u && m1 == 0xffu);
+        float y[kHalfT];
+        tmem_ld_partials16(tmem + lanes + kTmemS, y);
+        tmem_ld_partials16(tmem + lanes + kTmemS + 16u, y + 16);
+        tmem_ld_partials(tmem + lanes + kTmemS + 32u, y + 32);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.bar.s_free);
         float xmax = -INFINITY;
         if (all) {
 #pragma unroll
-          for (int j = 0; j < 48; ++j) {
+          for (int j = 0; j < kHalfT; ++j) {
             y[j] *= hs;
             xmax = fmaxf(xmax, y[j]);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 48; ++j) {
-            const bool there = ((j < 24 ? m0 >> j : m1 >> (j - 24)) & 1u) != 0u;
+          for (int j = 0; j < kHalfT; ++j) {
+            const bool there = ((j < 32 ? m0 >> j : m1 >> (j - 32)) & 1u) != 0u;
             y[j] = there ? y[j] * hs : -INFINITY;
             xmax = fmaxf(xmax, y[j]);
           }
@@ -671,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
         if (softmax_any(raise && had)) {
           if (ch == 0) sm.factor[h] = alpha;
           softmax_sync();
-          ok = mbar_wait_warp(&sm.bar.v_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag);
+          ok = wait_hot_warp(&sm.bar.v_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag);
           if (ok) {
             tc_fence_after();
 #pragma unroll 1
@@ -686,25 +779,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
           }
         }
         const float mm = m_ref == -INFINITY ? 0.0f : m_ref;   // nothing seen yet: 2^-inf = 0
-        const uint32_t prow = ps_s + (uint32_t)(buf * kPTile);
+        uint32_t w[kHalfT / 2];
 #pragma unroll
-        for (int k = 0; k < 6; ++k) {
-          uint32_t w[4];
+        for (int i = 0; i < kHalfT / 2; ++i) {
+          const float p0 = fast_exp2(y[2 * i] - mm), p1 = fast_exp2(y[2 * i + 1] - mm);
+          l += p0 + p1;
+          w[i] = pack_half2(p0, p1);
+        }
+        // P is free once O^T += of the tile before is complete
+        if (t > 0) ok = wait_hot_warp(&sm.bar.v_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float p0 = fast_exp2(y[8 * k + 2 * i] - mm);
-            const float p1 = fast_exp2(y[8 * k + 2 * i + 1] - mm);
-            l += p0 + p1;
-            w[i] = pack_half2(p0, p1);
-          }
-          const int c = 6 * ch + k;                 // 16-byte chunk: entries 8 c .. + 7
-          sts128(prow + (uint32_t)((c >> 3) * 8192 + swz(h, c & 7)),
-                 make_uint4(w[0], w[1], w[2], w[3]));
+        for (int k = 0; k < kHalfT / 8; ++k) {
+          const int c = (kHalfT / 8) * ch + k;      // 16-byte chunk: entries 8 c .. + 7
+          sts128(ps_s + (uint32_t)((c >> 3) * 8192 + swz(h, c & 7)),
+                 make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
         }
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.bar.p_full[buf]);
+        if (lane == 0) mbar_arrive(&sm.bar.p_full);
       }
       const float l_tot = l + __shfl_xor_sync(0xffffffffu, l, 16);
       if (ch == 0) sm.mlf[h] = make_float2(l_tot > 0.0f ? m_ref : -INFINITY, l_tot);
@@ -712,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
 
     // -------------------------------------------------------------- output
     bool have_o = false;
-    if (warp != kMmaWarp) have_o = mbar_wait_warp(&sm.bar.o_full, sph, abort_flag);
+    if (warp != kMmaWarp && warp != kLoadWarp) have_o = mbar_wait_warp(&sm.bar.o_full, sph, abort_flag);
     tc_fence_before();
     __syncthreads();                  // O^T is final, the (maximum, sum) pairs are in place
     tc_fence_after();
