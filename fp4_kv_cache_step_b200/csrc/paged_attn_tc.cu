@@ -4,21 +4,13 @@
 //
 // One entry is key and value; all heads share it. The query rows of a sequence
 // (its Tq tokens x Hq heads, contiguous) are taken in blocks of 64, the entries
-// in tiles of 96:
-//   S   = Q V^T    M = 64 rows, N = 96 entries, K = 512: Q is the A operand in
-//                  tensor memory, V the K-major B operand;
-//   O^T += V^T P^T M = 128 channels (four blocks of them), N = 64 rows, K = 96:
-//                  V is the MN-major A operand, P the K-major B operand.
-// Why these shapes (cycles per instruction of K = 16, measured on a B200 with
-// operands in place): M = 64 costs as much as M = 128, and no instruction takes
-// under 47: 47 at N = 64, 48.5 at N = 96, 65 at N = 128, 129 at N = 256. So O as
-// M = 64, N = 256 would take 16 cycles per entry, O^T takes 12; S takes 16.2 at
-// N = 96 (23.5 at N = 64). Two tiles of 96 entries x 512 channels of fp16 are
-// 192 KB, all that shared memory holds: one is filled while the other is used.
-// Tensor memory: O^T in columns 0-255 (all lanes); the query block's channels
-// 0-255 in lanes 0-15 of each quadrant and 256-511 in lanes 16-31, columns
-// 256-383; the two halves' partial logits in the same lanes, columns 384-479,
-// added when they are read.
+// in tiles of 80:
+//   S  = Q V^T   M = 64 rows, N = 80 entries, K = 512: Q is the A operand in
+//                tensor memory, V the K-major B operand;
+//   O += P V     M = 64 rows, N = 256 channels twice, K = 80: P is the K-major A
+//                operand, V the N-major B operand.
+// Tensor memory: lanes 0-15 of each quadrant hold two S buffers (columns 0-159)
+// and the query block (256-511), lanes 16-31 hold O (512 columns).
 //
 // Work is dealt out by tiles: the tiles of all (sequence, row block) pairs stand in
 // one line that is cut into as many equal pieces as there are SMs, so a ragged
@@ -26,13 +18,20 @@
 // one that is cut leaves fp32 partials with their (maximum, sum), which
 // paged_combine_kernel joins. A sequence without entries has one empty tile.
 //
-// Roles: warps 0-7 load codes and scales a tile ahead into registers, dequantise
-// (exact in fp16: at most 6 significant bits) and fill the tile, 12 entries each;
-// they also stage the query block. Warp 8 issues the MMAs. Warps 9-12 run the
-// softmax: a thread has one row's 48 entries of a tile. The reference maximum is
-// lazy (raised, with O^T's columns rescaled, only by a logit more than 8 above it
-// in log2 units), so P stays below 2^8 in fp16. All sums are fp32. Every wait is
-// bounded.
+// Roles. Warp 13 copies rows (288 bytes each, contiguous within a page) to shared
+// memory, two tiles ahead. Warps 0-7 dequantise them (exact in fp16: at most 6
+// significant bits) into the tile, channels 0-255 first; they also stage the query
+// block. Warp 8 issues the MMAs, two tiles at a time: S S PV PV, so that the
+// softmax of one tile runs beside S of the next, and a tile is filled again while
+// the other is multiplied. Warps 9-12 run the softmax, a thread having half of one
+// row's entries. The reference maximum is lazy (raised, with O rescaled, only by a
+// logit more than 8 above it in log2 units), so P stays below 2^8 in fp16. All
+// sums are fp32.
+// Warps hand work to each other through named barriers, which cost tens of cycles
+// where a waiting mbarrier's wake-up beside this shared-memory load cost 500 to
+// 800; what the tensor core or the copy engine signals are mbarriers, every wait
+// on one of which is bounded. Named barriers need no bound: each role passes every
+// one of them for every tile, whether or not a wait before it ran out.
 #include "common.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -48,7 +47,8 @@ constexpr int kT = 80;                     // entries of a tile
 constexpr int kHalfT = kT / 2;
 constexpr int kAtom = kT * 128;            // 80 entries x 64 channels of fp16
 constexpr int kVTile = 8 * kAtom;
-constexpr int kPTile = 2 * 8192;           // 64 rows x (64 + 16) entries of fp16, 128-byte rows
+constexpr int kP0 = 64 * 128;              // P, entries 0-63: rows of 128 bytes
+constexpr int kP1 = 64 * 32;               // P, entries 64-79: rows of 32 bytes
 constexpr int kRowBytes = kD / 2 + kD / 16;     // 288
 constexpr int kRawTile = kT * kRowBytes;
 constexpr int kProducerWarps = 8;
@@ -57,15 +57,31 @@ constexpr int kMmaWarp = 8;
 constexpr int kLoadWarp = 13;
 constexpr int kThreads = 14 * 32;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemQ = 256, kTmemS = 384;
+constexpr uint32_t kTmemQ = 256;
 constexpr uint32_t kHalfLanes = 16u << 16;      // lanes 16-31 of a quadrant
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleSlack = 8.0f;
 
+// Named barriers (0 is __syncthreads): who arrives -> who waits; all but the first
+// two once per tile, each role passing all of its own in order, so that none is
+// passed twice before its other side came by.
+enum : int {
+  kBarQ = 1,          // producers -> MMA, softmax: the query block is in tensor memory
+  kBarProducers = 2,  // among the producers
+  kBarP = 3,          // + buffer: softmax -> MMA: P is there
+  kBarL = 5,          // + buffer: loader -> producers: the copies are issued
+  kBarV = 7,          // + 2 buffer + half: producers -> MMA (and, second half, loader): filled
+  kBarF = 11,         // + buffer: MMA -> producers: O += of the tile is issued
+  kBarS = 13,         // + buffer: MMA -> softmax: S of the tile is issued
+};
+constexpr int kProducers = kProducerWarps * 32, kSoftmax = 4 * 32;
+constexpr int kNumQ = kProducers + 32 + kSoftmax, kNumP = kSoftmax + 32, kNumL = kProducers + 32;
+constexpr int kNumV0 = kProducers + 32, kNumV1 = kProducers + 64, kNumF = kProducers + 32;
+constexpr int kNumS = kSoftmax + 32;
+
 struct __align__(8) Bars {
-  uint64_t q_ld, q_conv, q_full, q_free, o_full, s_full, s_free;
-  uint64_t raw_full[2], raw_free[2], v_full[2], v_free[2], p_full;
+  uint64_t q_ld, o_full, s_full[2], raw_full[2], v_free[2][2];   // v_free: [tile][half]
 };
 
 struct Smem {
@@ -77,11 +93,10 @@ struct Smem {
   int first_b;
   uint32_t valid[4][3];             // bit i of a tile's 96: entry i is there
   float2 mlf[kRows];                // (reference maximum, row sum)
-  float factor[kRows];              // rescaling of each row
   float qdown[kRows];               // the power of two each row was scaled up by, inverted
 };
 
-constexpr size_t kSmemBytes = 1024 + 2 * kVTile + kPTile + 2 * kRawTile + sizeof(Smem);
+constexpr size_t kSmemBytes = 2 * kVTile + 2 * (kP0 + kP1) + 2 * kRawTile + sizeof(Smem);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 
 struct Params {
@@ -112,9 +127,16 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
   return d;
 }
 
-// kind::f16, F16 x F16 -> F32; A K-major (0) or M-major (1); B K-major.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn) {
-  return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)(N >> 3) << 17) |
+// the same for rows of 32 bytes with the 32-byte swizzle (16-byte chunk c of row r
+// at chunk c ^ (r >> 2 & 1)), 8-row groups of 256 bytes
+__device__ __forceinline__ uint64_t desc_sw32(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(256 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)6 << 61;
+}
+
+// kind::f16, F16 x F16 -> F32; A K-major; B K-major (0) or N-major (1).
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
 
@@ -175,6 +197,11 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 r;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
@@ -205,41 +232,29 @@ __device__ __forceinline__ uint4 dq8(uint32_t codes, __half2 scale) {
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-// The sum of 8 columns of the two partial logits of a row: threads 0-15 read
-// columns taddr .. + 7, threads 16-31 columns taddr + 40 .. + 47, of lanes 0-15
-// and 16-31 of the quadrant.
-__device__ __forceinline__ void tmem_ld_partials(uint32_t taddr, float* y) {
-  uint32_t a[8], b[8];
+// 40 columns of a row: threads 0-15 read columns taddr .. + 39 of lanes 0-15,
+// threads 16-31 columns taddr + 40 .. + 79.
+__device__ __forceinline__ void tmem_ld_logits(uint32_t taddr, float (&y)[kHalfT]) {
+  uint32_t a[kHalfT];
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16], %18;\n\t"
-      "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17], %18;\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
-        "=r"(a[7]), "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]),
-        "=r"(b[6]), "=r"(b[7])
-      : "r"(taddr), "r"(taddr + kHalfLanes), "n"(kHalfT)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
-}
-__device__ __forceinline__ void tmem_ld_partials16(uint32_t taddr, float* y) {
-  uint32_t a[16], b[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32], %34;\n\t"
-      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
-      "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33], %34;\n\t"
+      "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%40], 40;\n\t"
+      "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%32,%33,%34,%35,%36,%37,%38,%39}, [%41], 40;\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
         "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]),
-        "=r"(a[14]), "=r"(a[15]), "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]),
-        "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]),
-        "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
-      : "r"(taddr), "r"(taddr + kHalfLanes), "n"(kHalfT)
+        "=r"(a[14]), "=r"(a[15]), "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]),
+        "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]), "=r"(a[24]), "=r"(a[25]),
+        "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31]),
+        "=r"(a[32]), "=r"(a[33]), "=r"(a[34]), "=r"(a[35]), "=r"(a[36]), "=r"(a[37]),
+        "=r"(a[38]), "=r"(a[39])
+      : "r"(taddr), "r"(taddr + 32u)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
+  for (int i = 0; i < kHalfT; ++i) y[i] = __uint_as_float(a[i]);
 }
+static_assert(kHalfT == 40, "the loads above");
 
 // mbar_wait without its sleeps: the hardware suspends the thread in try_wait
 // (up to a microsecond at a time), and wakes it with the phase
@@ -270,19 +285,11 @@ __device__ __forceinline__ bool wait_hot_warp(uint64_t* bar, uint32_t parity, vo
   return __all_sync(0xffffffffu, ok) != 0;
 }
 
-// Whether any of the softmax threads says so (also a barrier among them).
-__device__ __forceinline__ bool softmax_any(bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)x)
-      : "memory");
-  return r != 0;
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-__device__ __forceinline__ void softmax_sync() {
-  asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // ---------------------------------------------------------------- lengths, pieces
@@ -317,12 +324,9 @@ __device__ __forceinline__ int piece_of(long long tile, int pieces, long long to
 }
 
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params p) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  uint8_t* vs = base;                          // [2][8 atoms][80 entries][128 B]
-  uint8_t* ps = vs + 2 * kVTile;               // [2 atoms][64 rows][128 B]
-  uint8_t* raw = ps + kPTile;                  // [2][80 entries][288 B]
+  extern __shared__ __align__(1024) uint8_t vs[];   // [2][8 atoms][80 entries][128 B]
+  uint8_t* ps = vs + 2 * kVTile;               // [2][64 rows][128 B], [2][64 rows][32 B]
+  uint8_t* raw = ps + 2 * (kP0 + kP1);         // [2][80 entries][288 B]
   Smem& sm = *reinterpret_cast<Smem*>(raw + 2 * kRawTile);
   volatile int* abort_flag = &sm.abort_flag;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
@@ -330,19 +334,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
 
   if (threadIdx.x == 0) {
     mbar_init(&sm.bar.q_ld, 1);
-    mbar_init(&sm.bar.q_conv, kProducerWarps);
-    mbar_init(&sm.bar.q_full, kProducerWarps);
-    mbar_init(&sm.bar.q_free, kProducerWarps);
     mbar_init(&sm.bar.o_full, 1);
-    mbar_init(&sm.bar.s_full, 1);
-    mbar_init(&sm.bar.s_free, 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.bar.v_full[i], kProducerWarps);
-      mbar_init(&sm.bar.v_free[i], 1);
+      mbar_init(&sm.bar.s_full[i], 1);
       mbar_init(&sm.bar.raw_full[i], 1);
-      mbar_init(&sm.bar.raw_free[i], kProducerWarps);
+      mbar_init(&sm.bar.v_free[i][0], 1);
+      mbar_init(&sm.bar.v_free[i][1], 1);
     }
-    mbar_init(&sm.bar.p_full, 4);
     sm.abort_flag = 0;
     fence_mbar_init();
   }
@@ -404,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
   long long seq_base = sm.base;
   int b = sm.first_b;
 
-  const uint32_t vs_s = smem_u32(vs), ps_s = smem_u32(ps);
+  const uint32_t vs_s = smem_u32(vs), ps_s = smem_u32(ps);   // 1024-byte aligned, as swizzles need
   const int quad = warp & 3;
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
   uint32_t g0 = 0;                  // tiles of this CTA before the current segment
@@ -446,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
       // tensor memory, thread (row, channel half) of two warps per quadrant
       auto stage_q = [&]() {
         const uint32_t qsm = vs_s + (uint32_t)(qbuf * kVTile);
-        bool ok = mbar_wait_warp(&sm.bar.q_ld, sph, abort_flag);
+        const bool ok = wait_hot_warp(&sm.bar.q_ld, sph, abort_flag);
         if (ok) {
 #pragma unroll 1
           for (int i0 = 0; i0 < 8; i0 += 2) {
@@ -490,74 +488,78 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
             }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.bar.q_conv);
-        ok = mbar_wait_warp(&sm.bar.q_conv, sph, abort_flag) && ok;
+        bar_sync(kBarProducers, kProducers);
         const int h = quad * 16 + u;
 #pragma unroll 1
         for (int i = 2 * (warp >> 2); i < 2 * (warp >> 2) + 2; ++i) {
-          float pk[32];
+          uint32_t w[32];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             uint4 v = make_uint4(0, 0, 0, 0);
             if (ok && h < nr)
               v = lds128(qsm + h * 1024 + (((32 * half + 8 * i + j) ^ (h & 7)) << 4));
-            pk[4 * j] = __uint_as_float(v.x);
-            pk[4 * j + 1] = __uint_as_float(v.y);
-            pk[4 * j + 2] = __uint_as_float(v.z);
-            pk[4 * j + 3] = __uint_as_float(v.w);
+            w[4 * j] = v.x;
+            w[4 * j + 1] = v.y;
+            w[4 * j + 2] = v.z;
+            w[4 * j + 3] = v.w;
           }
-          // lanes 0-15: channels 64 i .. + 63; lanes 16-31: 256 further
-          tmem_st_32(tmem + lanes + kTmemQ + 32u * i, pk);
+          // threads 0-15: channels 64 i .. + 63; threads 16-31: 256 further
+          tmem_st16x2_32<128>(tmem + lanes + kTmemQ + 32u * i, w);
         }
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.bar.q_full);
-          mbar_arrive(&sm.bar.q_free);
-        }
+        bar_sync(kBarProducers, kProducers);     // the block is read: its tile can be filled
+        bar_arrive(kBarQ, kNumQ);
+        return ok;
       };
 
-      stage_q();
+      bool ok = stage_q();
       for (int t = 0; t < nt; ++t) {
         const uint32_t g = g0 + t;
         const int buf = (int)(g & 1);
         const uint32_t ph = (g >> 1) & 1;
-        if (!wait_hot_warp(&sm.bar.raw_full[buf], ph, abort_flag)) break;
-        if (!wait_hot_warp(&sm.bar.v_free[buf], ph ^ 1, abort_flag)) break;
-        if (t == 1 && !wait_hot_warp(&sm.bar.q_free, sph, abort_flag)) break;
-        const uint32_t tile = vs_s + (uint32_t)(buf * kVTile);
-        const uint32_t rows = smem_u32(raw) + (uint32_t)(buf * kRawTile);
+        bar_sync(kBarL + buf, kNumL);
+        ok = ok && wait_hot_warp(&sm.bar.raw_full[buf], ph, abort_flag);
+        if (t >= 2) bar_sync(kBarF + buf, kNumF);
         const uint32_t* valid = sm.valid[g & 3];
-#pragma unroll
-        for (int r = 0; r < kPerWarp / 2; ++r) {
-          const int e = warp * kPerWarp + 2 * r + half;
-          const uint32_t row = rows + (uint32_t)(e * kRowBytes);
-          uint2 c0 = lds64(row + 8 * u), c1 = lds64(row + 128 + 8 * u);
-          uint32_t s0 = lds8(row + 256 + u), s1 = lds8(row + 272 + u);
-          if (!(valid[e >> 5] >> (e & 31) & 1u)) {      // nothing was copied there
-            c0 = c1 = make_uint2(0, 0);
-            s0 = s1 = 0;
-          }
-          const __half2 f0 = e4m3x2_to_half2((uint16_t)(s0 * 0x0101u));
-          const __half2 f1 = e4m3x2_to_half2((uint16_t)(s1 * 0x0101u));
+        // channels 0-255, then 256-511: each half is freed, filled and multiplied
+        // on its own, so that S starts when half a tile is there
+#pragma unroll 1
+        for (int hh = 0; hh < 2; ++hh) {
           // channels 256 hh + 16 u: atom 4 hh + u / 4, 16-byte chunks 2 (u % 4), + 1
-          const uint32_t a0 = tile + (uint32_t)((u >> 2) * kAtom), a1 = a0 + 4u * kAtom;
-          // lanes u and u + 4 would meet in one bank group: every other four take
-          // their two chunks in the other order
-          const int odd = (u >> 2) & 1, c = (u & 3) * 2 + odd;
-          sts128(a0 + swz(e, c), dq8(odd ? c0.y : c0.x, f0));
-          sts128(a0 + swz(e, c ^ 1), dq8(odd ? c0.x : c0.y, f0));
-          sts128(a1 + swz(e, c), dq8(odd ? c1.y : c1.x, f1));
-          sts128(a1 + swz(e, c ^ 1), dq8(odd ? c1.x : c1.y, f1));
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.bar.v_full[buf]);
-          mbar_arrive(&sm.bar.raw_free[buf]);
+          const uint32_t a0 = vs_s + (uint32_t)(buf * kVTile + (4 * hh + (u >> 2)) * kAtom);
+          const uint32_t rows = smem_u32(raw) + (uint32_t)(buf * kRawTile);
+          uint2 c[kPerWarp / 2];
+          uint32_t sc[kPerWarp / 2];
+          if (ok) {
+#pragma unroll
+            for (int r = 0; r < kPerWarp / 2; ++r) {
+              const uint32_t row = rows + (uint32_t)((warp * kPerWarp + 2 * r + half) * kRowBytes);
+              c[r] = lds64(row + 128 * hh + 8 * u);
+              sc[r] = lds8(row + 256 + 16 * hh + u);
+            }
+          }
+          ok = ok && wait_hot_warp(&sm.bar.v_free[buf][hh], ph ^ 1, abort_flag);
+          if (ok) {
+#pragma unroll
+            for (int r = 0; r < kPerWarp / 2; ++r) {
+              const int e = warp * kPerWarp + 2 * r + half;
+              if (!(valid[e >> 5] >> (e & 31) & 1u)) {      // nothing was copied there
+                c[r] = make_uint2(0, 0);
+                sc[r] = 0;
+              }
+              const __half2 f = e4m3x2_to_half2((uint16_t)(sc[r] * 0x0101u));
+              // lanes u and u + 4 would meet in one bank group: every other four
+              // take their two chunks in the other order
+              const int odd = (u >> 2) & 1, k = (u & 3) * 2 + odd;
+              sts128(a0 + swz(e, k), dq8(odd ? c[r].y : c[r].x, f));
+              sts128(a0 + swz(e, k ^ 1), dq8(odd ? c[r].x : c[r].y, f));
+            }
+          }
+          fence_async_smem();
+          bar_arrive(kBarV + 2 * buf + hh, hh ? kNumV1 : kNumV0);
         }
       }
+      for (int t = max(0, nt - 2); t < nt; ++t) bar_sync(kBarF + (int)((g0 + t) & 1), kNumF);
     } else if (warp == kLoadWarp) {
       // ---------------------------------------------------------- bulk copies
       // Lane i copies the rows of a tile that lie in its i-th page (a tile of 80
@@ -598,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
           const uint32_t m = (x1 >= 32 ? ~0u : (1u << x1) - 1u) & ~(x0 >= 32 ? ~0u : (1u << x0) - 1u);
           bits[w] = __reduce_or_sync(0xffffffffu, count ? m : 0u);
         }
-        if (!wait_hot_warp(&sm.bar.raw_free[buf], ((g >> 1) & 1) ^ 1, abort_flag)) break;
+        if (t >= 2) bar_sync(kBarV + 2 * buf + 1, kNumV1);     // the rows before are read
         if (lane == 0) {
 #pragma unroll
           for (int w = 0; w < 3; ++w) sm.valid[g & 3][w] = bits[w];
@@ -611,87 +613,75 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
           bulk_load(raw + buf * kRawTile + at * kRowBytes,
                     p.pg.rows + (((size_t)place << p.shift) + (size_t)(lo & (p.pg.page - 1))) * kRowBytes,
                     (uint32_t)count * kRowBytes, &sm.bar.raw_full[buf]);
+        bar_arrive(kBarL + buf, kNumL);
         place = place_next;
       }
+      for (int t = max(0, nt - 2); t < nt; ++t)
+        bar_sync(kBarV + 2 * (int)((g0 + t) & 1) + 1, kNumV1);
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMA issuer
       // The whole warp runs this with warp-uniform values and one elected lane
       // issues: descriptors then stay in uniform registers (from one divergent
       // thread an instruction took 65 to 80 cycles to issue, more than to run).
       const uint32_t id_s = idesc_f16(64, kT, 0);
-      const uint32_t id_o = idesc_f16(128, kRows, 1);
+      const uint32_t id_o = idesc_f16(64, 256, 1);
       const uint64_t vk = desc_sw128(vs_s, 16, 1024);       // V as K-major B
-      const uint64_t vm = desc_sw128(vs_s, kAtom, 1024);    // V as M-major A
-      const uint64_t pk = desc_sw128(ps_s, 16, 1024);       // P as K-major B
+      const uint64_t vn = desc_sw128(vs_s, kAtom, 1024);    // V as N-major B
+      const uint64_t p0 = desc_sw128(ps_s, 16, 1024);       // P as K-major A
+      const uint64_t p1 = desc_sw32(ps_s + 2 * kP0);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t gu = __shfl_sync(0xffffffffu, g0, 0);
       const int ntu = __shfl_sync(0xffffffffu, nt, 0);
-      bool ok = wait_hot_warp(&sm.bar.q_full, sph, abort_flag);
-      tc_fence_after();
-      auto issue_s = [&](uint32_t buf) {
+      bar_sync(kBarQ, kNumQ);
+      auto issue_s = [&](uint32_t buf, int hh) {
         tc_fence_after();
-        const uint64_t v = vk + (uint64_t)((buf * kVTile) >> 4);
+        const uint64_t v = vk + (uint64_t)((buf * kVTile + hh * 4 * kAtom) >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 16; ++k)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-              mma_ts(tm + hf * kHalfLanes + kTmemS, tm + hf * kHalfLanes + kTmemQ + 8u * k,
-                     v + (uint64_t)(((4 * hf + (k >> 2)) * kAtom + (k & 3) * 32) >> 4), id_s,
-                     k > 0 ? 1u : 0u);
-          mma_commit(&sm.bar.s_full);
+            mma_ts(tm + (uint32_t)kT * buf, tm + kTmemQ + 128u * hh + 8u * k,
+                   v + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), id_s,
+                   k > 0 || hh > 0 ? 1u : 0u);
+          if (hh == 1) mma_commit(&sm.bar.s_full[buf]);
         }
         __syncwarp();
       };
       auto issue_pv = [&](uint32_t buf, uint32_t acc0) {
         tc_fence_after();
-        const uint64_t v = vm + (uint64_t)((buf * kVTile) >> 4);
+        const uint64_t v = vn + (uint64_t)((buf * kVTile) >> 4);
+        const uint64_t a0 = p0 + (uint64_t)((buf * kP0) >> 4);
+        const uint64_t a1 = p1 + (uint64_t)((buf * kP1) >> 4);
         if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
             for (int ks = 0; ks < kT / 16; ++ks)
-              mma_ss(tm + 64u * j, v + (uint64_t)((2 * j * kAtom + ks * 2048) >> 4),
-                     pk + (uint64_t)(((ks >> 2) * 8192 + (ks & 3) * 32) >> 4), id_o,
-                     ks > 0 ? 1u : acc0);
-          mma_commit(&sm.bar.v_free[buf]);
+              mma_ss(tm + kHalfLanes + 256u * hh, ks < 4 ? a0 + (uint64_t)(ks * 32 >> 4) : a1,
+                     v + (uint64_t)((4 * hh * kAtom + ks * 2048) >> 4), id_o, ks > 0 ? 1u : acc0);
+            mma_commit(&sm.bar.v_free[buf][hh]);
+          }
         }
         __syncwarp();
       };
-      auto done = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) != 0;
-      };
-      // whichever is ready first: S of a tile (filled, and the logits before it
-      // read) or O^T += of a tile (its P published)
-      int next_s = 0, next_pv = 0;
-      uint64_t t_last = 0;
-      uint32_t spins = 0;
-      while (ok && next_pv < ntu) {
-        bool did = false;
-        const uint32_t gs = gu + next_s, gp = gu + next_pv;
-        if (next_s < ntu && done(&sm.bar.s_free, (gs & 1) ^ 1) &&
-            done(&sm.bar.v_full[gs & 1], (gs >> 1) & 1)) {
-          issue_s(gs & 1);
-          ++next_s;
-          did = true;
-        }
-        if (next_pv < next_s && done(&sm.bar.p_full, gp & 1)) {
-          issue_pv(gp & 1, next_pv > 0 ? 1u : 0u);
-          ++next_pv;
-          did = true;
-        }
-        if (did) {
-          spins = 0;
-        } else {
-          __nanosleep(20);
-          if ((++spins & 63u) == 0u) {
-            const uint64_t now = global_ns();
-            if (spins == 64u) t_last = now;
-            if (__any_sync(0xffffffffu, *abort_flag != 0 || now - t_last > kWaitLimitNs)) {
-              *abort_flag = 1;
-              ok = false;
-            }
+      for (int t = 0; t < ntu; t += 2) {
+        const int more = min(2, ntu - t);
+        const bool go = !__any_sync(0xffffffffu, *abort_flag != 0);
+#pragma unroll 1
+        for (int i = 0; i < more; ++i) {
+          const uint32_t buf = (gu + t + i) & 1;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            bar_sync(kBarV + 2 * buf + hh, hh ? kNumV1 : kNumV0);
+            if (go) issue_s(buf, hh);
           }
+          bar_arrive(kBarS + buf, kNumS);
+        }
+#pragma unroll 1
+        for (int i = 0; i < more; ++i) {
+          const uint32_t buf = (gu + t + i) & 1;
+          bar_sync(kBarP + buf, kNumP);
+          if (go) issue_pv(buf, t + i > 0 ? 1u : 0u);
+          bar_arrive(kBarF + buf, kNumF);
         }
       }
       if (elect_one()) mma_commit(&sm.bar.o_full);
@@ -699,105 +689,101 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
       // nothing may be in flight when tensor memory is reused or released
       wait_hot_warp(&sm.bar.o_full, sph, abort_flag);
     } else {
-      // ---------------------------------------------------------- softmax (warps 9-12)
+      // ---------------------------------------------------------- softmax
       const int hl = lane & 15, ch = lane >> 4;
       const int h = quad * 16 + hl;
-      bool ok = mbar_wait_warp(&sm.bar.q_full, sph, abort_flag);
+      bar_sync(kBarQ, kNumQ);
       const bool real = h < nr;
-      const float hs = ok && real ? p.softmax_scale * kLog2e * sm.qdown[h] : 0.0f;
+      const float hs = real ? p.softmax_scale * kLog2e * sm.qdown[h] : 0.0f;
       // entries that this row sees
       const int n_row = real ? (p.nvalid ? visible(p, b, (r0 + h) / p.Hq, false) : n_most) : n_most;
+      bool ok = true;
       for (int t = 0; t < nt; ++t) {
         const uint32_t g = g0 + t;
         const int buf = (int)(g & 1);
-        ok = ok && wait_hot_warp(&sm.bar.v_full[buf], (g >> 1) & 1, abort_flag) &&
-             wait_hot_warp(&sm.bar.s_full, g & 1, abort_flag);
-        // every softmax warp takes part in the barriers below, or none does
-        if (softmax_any(!ok)) break;
-        tc_fence_after();
-        // this thread's entries: 40 ch .. + 39 of the tile, masks of 32 and 8
-        const int left = n_row - (t0 + t) * kT - kHalfT * ch;
-        uint32_t m0, m1;
-        {
-          const uint32_t* v = sm.valid[g & 3];
-          m0 = ch ? (v[1] >> 8) | (v[2] << 24) : v[0];
-          m1 = (ch ? v[2] >> 8 : v[1]) & 0xffu;
-          if (left < kHalfT) {
-            m0 &= left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1u;
-            m1 &= left <= 32 ? 0u : (1u << (left - 32)) - 1u;
-          }
-        }
-        const bool all = __all_sync(0xffffffffu, m0 == ~0u && m1 == 0xffu);
-        float y[kHalfT];
-        tmem_ld_partials16(tmem + lanes + kTmemS, y);
-        tmem_ld_partials16(tmem + lanes + kTmemS + 16u, y + 16);
-        tmem_ld_partials(tmem + lanes + kTmemS + 32u, y + 32);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.bar.s_free);
-        float xmax = -INFINITY;
-        if (all) {
-#pragma unroll
-          for (int j = 0; j < kHalfT; ++j) {
-            y[j] *= hs;
-            xmax = fmaxf(xmax, y[j]);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < kHalfT; ++j) {
-            const bool there = ((j < 32 ? m0 >> j : m1 >> (j - 32)) & 1u) != 0u;
-            y[j] = there ? y[j] * hs : -INFINITY;
-            xmax = fmaxf(xmax, y[j]);
-          }
-        }
-        xmax = fmaxf(xmax, __shfl_xor_sync(0xffffffffu, xmax, 16));
-        const bool raise = xmax > m_ref + kRescaleSlack;
-        const bool had = m_ref != -INFINITY;
-        float alpha = 1.0f;
-        if (raise) {
-          alpha = had ? fast_exp2(m_ref - xmax) : 1.0f;
-          m_ref = xmax;
-          l *= alpha;
-        }
-        // O^T's columns are rows of the query block, its lanes channels: a warp
-        // rescales its lanes for all rows
-        if (softmax_any(raise && had)) {
-          if (ch == 0) sm.factor[h] = alpha;
-          softmax_sync();
-          ok = wait_hot_warp(&sm.bar.v_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag);
-          if (ok) {
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              float o[32];
-              tmem_ld_32(tmem + lanes + 32u * c, o);
-              const float* f = sm.factor + 32 * (c & 1);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= f[i];
-              tmem_st_32(tmem + lanes + 32u * c, o);
+        bar_sync(kBarS + buf, kNumS);
+        ok = ok && wait_hot_warp(&sm.bar.s_full[buf], (g >> 1) & 1, abort_flag);
+        if (ok) {
+          tc_fence_after();
+          // this thread's entries: 40 ch .. + 39 of the tile, masks of 32 and 8
+          const int left = n_row - (t0 + t) * kT - kHalfT * ch;
+          uint32_t m0, m1;
+          {
+            const uint32_t* v = sm.valid[g & 3];
+            m0 = ch ? (v[1] >> 8) | (v[2] << 24) : v[0];
+            m1 = (ch ? v[2] >> 8 : v[1]) & 0xffu;
+            if (left < kHalfT) {
+              m0 &= left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1u;
+              m1 &= left <= 32 ? 0u : (1u << (left - 32)) - 1u;
             }
           }
-        }
-        const float mm = m_ref == -INFINITY ? 0.0f : m_ref;   // nothing seen yet: 2^-inf = 0
-        uint32_t w[kHalfT / 2];
+          float y[kHalfT];
+          tmem_ld_logits(tmem + lanes + (uint32_t)kT * buf, y);
+          float xmax = -INFINITY;
+          if (__all_sync(0xffffffffu, m0 == ~0u && m1 == 0xffu)) {
 #pragma unroll
-        for (int i = 0; i < kHalfT / 2; ++i) {
-          const float p0 = fast_exp2(y[2 * i] - mm), p1 = fast_exp2(y[2 * i + 1] - mm);
-          l += p0 + p1;
-          w[i] = pack_half2(p0, p1);
-        }
-        // P is free once O^T += of the tile before is complete
-        if (t > 0) ok = wait_hot_warp(&sm.bar.v_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag);
+            for (int j = 0; j < kHalfT; ++j) {
+              y[j] *= hs;
+              xmax = fmaxf(xmax, y[j]);
+            }
+          } else {
 #pragma unroll
-        for (int k = 0; k < kHalfT / 8; ++k) {
-          const int c = (kHalfT / 8) * ch + k;      // 16-byte chunk: entries 8 c .. + 7
-          sts128(ps_s + (uint32_t)((c >> 3) * 8192 + swz(h, c & 7)),
-                 make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+            for (int j = 0; j < kHalfT; ++j) {
+              const bool there = ((j < 32 ? m0 >> j : m1 >> (j - 32)) & 1u) != 0u;
+              y[j] = there ? y[j] * hs : -INFINITY;
+              xmax = fmaxf(xmax, y[j]);
+            }
+          }
+          xmax = fmaxf(xmax, __shfl_xor_sync(0xffffffffu, xmax, 16));
+          const bool raise = xmax > m_ref + kRescaleSlack;
+          if (__any_sync(0xffffffffu, raise)) {
+            float alpha = 1.0f;
+            if (raise) {
+              if (m_ref != -INFINITY) alpha = fast_exp2(m_ref - xmax);
+              m_ref = xmax;
+              l *= alpha;
+            }
+            // O holds the tiles before: rescaled once they are complete (O += of
+            // this one waits for its P)
+            if (t > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+              const uint32_t gb = g - 1;
+              ok = wait_hot_warp(&sm.bar.v_free[gb & 1][1], (gb >> 1) & 1, abort_flag);
+              if (ok) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int c0 = 0; c0 < kD / 2; c0 += 32) {
+                  float o[32];
+                  tmem_ld16x2_32<256>(tmem + lanes + kHalfLanes + c0, o);
+                  uint32_t ow[32];
+#pragma unroll
+                  for (int c = 0; c < 32; ++c) ow[c] = __float_as_uint(o[c] * alpha);
+                  tmem_st16x2_32<256>(tmem + lanes + kHalfLanes + c0, ow);
+                }
+              }
+            }
+          }
+          const float mm = m_ref == -INFINITY ? 0.0f : m_ref;   // nothing seen yet: 2^-inf = 0
+#pragma unroll
+          for (int k = 0; k < kHalfT / 8; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float x0 = fast_exp2(y[8 * k + 2 * i] - mm);
+              const float x1 = fast_exp2(y[8 * k + 2 * i + 1] - mm);
+              l += x0 + x1;
+              w[i] = pack_half2(x0, x1);
+            }
+            const int c = (kHalfT / 8) * ch + k;      // 16-byte chunk: entries 8 c .. + 7
+            const uint32_t at =
+                c < 8 ? ps_s + (uint32_t)(buf * kP0 + swz(h, c))
+                      : ps_s + (uint32_t)(2 * kP0 + buf * kP1 + h * 32 +
+                                          (((c - 8) ^ (h >> 2 & 1)) << 4));
+            sts128(at, make_uint4(w[0], w[1], w[2], w[3]));
+          }
+          fence_async_smem();
+          tc_fence_before();
         }
-        fence_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.bar.p_full);
+        bar_arrive(kBarP + buf, kNumP);
       }
       const float l_tot = l + __shfl_xor_sync(0xffffffffu, l, 16);
       if (ch == 0) sm.mlf[h] = make_float2(l_tot > 0.0f ? m_ref : -INFINITY, l_tot);
@@ -810,42 +796,40 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
     __syncthreads();                  // O^T is final, the (maximum, sum) pairs are in place
     tc_fence_after();
     if (have_o) {
-      // chunks of 32 columns (32 rows of one block of 128 channels): the
-      // quadrant's softmax warp takes two, its producer warps three each
-      const int cb = warp > kMmaWarp ? 0 : warp < 4 ? 2 : 5;
-      const int ce = warp > kMmaWarp ? 2 : warp < 4 ? 5 : 8;
+      const int hl = lane & 15, ch = lane >> 4, h = quad * 16 + hl;
+      const float2 ml = sm.mlf[h];
+      // chunks of 32 columns (and the same 256 further): the quadrant's softmax
+      // warp takes 0-2, its producer warps 3-5 and 6-7
+      const int cb = warp > kMmaWarp ? 0 : warp < 4 ? 3 : 6;
+      const int ce = warp > kMmaWarp ? 3 : warp < 4 ? 6 : 8;
 #pragma unroll 1
       for (int c = cb; c < ce; ++c) {
         float o[32];
-        tmem_ld_32(tmem + lanes + 32u * c, o);
-        const int d = 128 * (c >> 1) + quad * 32 + lane, h0 = 32 * (c & 1);
+        tmem_ld16x2_32<256>(tmem + lanes + kHalfLanes + 32u * c, o);
+        if (h >= nr) continue;
+        const int d0 = 256 * ch + 32 * c;           // this thread's channels d0 .. + 31
+        // (a row that saw nothing has sum 0 and zeros in O)
         if (whole) {
-          uint16_t* dst = p.out + (row0 + h0) * kD + d;
+          const float f = ml.y > 0.0f ? 1.0f / ml.y : 0.0f;
+          uint4* dst = reinterpret_cast<uint4*>(p.out + (row0 + h) * kD + d0);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (h0 + i >= nr) break;
-            const float lt = sm.mlf[h0 + i].y;
-            const __nv_bfloat16 x = __float2bfloat16_rn(lt > 0.0f ? o[i] / lt : 0.0f);
-            dst[(size_t)i * kD] = *reinterpret_cast<const uint16_t*>(&x);
-          }
+          for (int k = 0; k < 4; ++k)
+            dst[k] = make_uint4(pack_bf162(o[8 * k] * f, o[8 * k + 1] * f),
+                                pack_bf162(o[8 * k + 2] * f, o[8 * k + 3] * f),
+                                pack_bf162(o[8 * k + 4] * f, o[8 * k + 5] * f),
+                                pack_bf162(o[8 * k + 6] * f, o[8 * k + 7] * f));
         } else {
-          float* dst = p.ws_o + ((size_t)slot * kRows + h0) * kD + d;
+          float4* dst = reinterpret_cast<float4*>(p.ws_o + ((size_t)slot * kRows + h) * kD + d0);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (h0 + i >= nr) break;
-            dst[(size_t)i * kD] = sm.mlf[h0 + i].y > 0.0f ? o[i] : 0.0f;
-          }
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
       }
-      if (warp > kMmaWarp && lane < 16) {
-        const int h = quad * 16 + lane;
-        const float2 ml = sm.mlf[h];
-        if (h < nr) {
-          if (!whole)
-            p.ws_ml[(size_t)slot * kRows + h] = ml;
-          else if (p.lse)
-            p.lse[row0 + h] = ml.y > 0.0f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
-        }
+      if (warp > kMmaWarp && ch == 0 && h < nr) {
+        if (!whole)
+          p.ws_ml[(size_t)slot * kRows + h] = ml;
+        else if (p.lse)
+          p.lse[row0 + h] = ml.y > 0.0f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
       }
     }
     tc_fence_before();
