@@ -18,12 +18,12 @@
 // one that is cut leaves fp32 partials with their (maximum, sum), which
 // paged_combine_kernel joins. A sequence without entries has one empty tile.
 //
-// Roles. Warp 13 copies rows (288 bytes each, contiguous within a page) to shared
-// memory, two tiles ahead. Warps 0-7 dequantise them (exact in fp16: at most 6
-// significant bits) into the tile, channels 0-255 first; they also stage the query
-// block. Warp 8 issues the MMAs, two tiles at a time: S S PV PV, so that the
+// Roles. Warp 15 copies rows (288 bytes each, contiguous within a page) to shared
+// memory, two tiles ahead. Warps 0-9 dequantise them (exact in fp16: at most 6
+// significant bits) into the tile, channels 0-255 first; 0-7 also stage the query
+// block. Warp 14 issues the MMAs, two tiles at a time: S S PV PV, so that the
 // softmax of one tile runs beside S of the next, and a tile is filled again while
-// the other is multiplied. Warps 9-12 run the softmax, a thread having half of one
+// the other is multiplied. Warps 10-13 run the softmax, a thread having half of one
 // row's entries. The reference maximum is lazy (raised, with O rescaled, only by a
 // logit more than 8 above it in log2 units), so P stays below 2^8 in fp16. All
 // sums are fp32.
@@ -51,11 +51,10 @@ constexpr int kP0 = 64 * 128;              // P, entries 0-63: rows of 128 bytes
 constexpr int kP1 = 64 * 32;               // P, entries 64-79: rows of 32 bytes
 constexpr int kRowBytes = kD / 2 + kD / 16;     // 288
 constexpr int kRawTile = kT * kRowBytes;
-constexpr int kProducerWarps = 8;
-constexpr int kPerWarp = kT / kProducerWarps;   // 10 entries of a tile per producer warp
-constexpr int kMmaWarp = 8;
-constexpr int kLoadWarp = 13;
-constexpr int kThreads = 14 * 32;
+constexpr int kProducerWarps = 10;         // 8 entries of a tile each
+constexpr int kMmaWarp = 14;
+constexpr int kLoadWarp = 15;
+constexpr int kThreads = 16 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemQ = 256;
 constexpr uint32_t kHalfLanes = 16u << 16;      // lanes 16-31 of a quadrant
@@ -72,26 +71,25 @@ enum : int {
   kBarP = 3,          // + buffer: softmax -> MMA: P is there
   kBarL = 5,          // + buffer: loader -> producers: the copies are issued
   kBarV = 7,          // + 2 buffer + half: producers -> MMA (and, second half, loader): filled
-  kBarF = 11,         // + buffer: MMA -> producers: O += of the tile is issued
-  kBarS = 13,         // + buffer: MMA -> softmax: S of the tile is issued
+  kBarS = 11,         // + buffer: MMA -> softmax: S of the tile is issued
 };
 constexpr int kProducers = kProducerWarps * 32, kSoftmax = 4 * 32;
 constexpr int kNumQ = kProducers + 32 + kSoftmax, kNumP = kSoftmax + 32, kNumL = kProducers + 32;
-constexpr int kNumV0 = kProducers + 32, kNumV1 = kProducers + 64, kNumF = kProducers + 32;
+constexpr int kNumV0 = kProducers + 32, kNumV1 = kProducers + 64;
 constexpr int kNumS = kSoftmax + 32;
 
 struct __align__(8) Bars {
   uint64_t q_ld, o_full, s_full[2], raw_full[2], v_free[2][2];   // v_free: [tile][half]
 };
 
-struct Smem {
+struct __align__(16) Smem {
   Bars bar;
   uint32_t tmem_slot;
   int abort_flag;
   long long base;                   // tiles before the first sequence of this piece
   long long total;                  // tiles in all
   int first_b;
-  uint32_t valid[4][3];             // bit i of a tile's 96: entry i is there
+  uint4 valid[4];                   // bit i of a tile's 128: entry i is there
   float2 mlf[kRows];                // (reference maximum, row sum)
   float qdown[kRows];               // the power of two each row was scaled up by, inverted
 };
@@ -202,14 +200,9 @@ __device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 r;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
-  return r;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t r;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a));
   return r;
 }
 
@@ -406,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
   const int quad = warp & 3;
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
   uint32_t g0 = 0;                  // tiles of this CTA before the current segment
+  uint32_t used[2] = {0, 0};        // ... by buffer (a segment starts with buffer 0)
   const long long piece_first = pos;
 
   for (uint32_t sg = 0; pos < end; ++sg) {
@@ -422,7 +416,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
     const int nr = min(kRows, p.Tq * p.Hq - r0);
     const size_t row0 = (size_t)b * p.Tq * p.Hq + r0;
     const uint32_t sph = sg & 1;                           // phase of the per-segment barriers
-    const int qbuf = (int)((g0 + 1) & 1);                  // the tile that holds the query block first
     if (threadIdx.x == 0) {
       if (t0 == 0) {
         const int first = piece, last = piece_of(pair_base + tiles - 1, pieces, total);
@@ -430,24 +423,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
       }
       const uint32_t qbytes = (uint32_t)nr * kD * 2;
       mbar_arrive_expect_tx(&sm.bar.q_ld, qbytes);
-      bulk_load(vs + qbuf * kVTile, p.q + row0 * kD, qbytes, &sm.bar.q_ld);
+      bulk_load(vs + kVTile, p.q + row0 * kD, qbytes, &sm.bar.q_ld);   // the second tile, for now
     }
     float m_ref = -INFINITY, l = 0.0f;
 
     if (warp < kProducerWarps) {
       // ---------------------------------------------------------- load + dequantise
-      // Lane 16 j + u takes channels 16u .. + 15 and 256 + 16u .. + 15 of entries
-      // 10 w + 2 r + j of a tile, r = 0 .. 4: whole lines of two rows at a time.
-      const int u = lane & 15, half = lane >> 4;
+      // Eight lanes take one half (256 channels) of a row: the lane with (i, j) the
+      // 32 channels 256 hh + 32 j .. of entry 8 w + 4 k + i of a tile, k = 0, 1.
+      // Eight neighbouring lanes have four rows and two neighbouring j: rows lie
+      // 288 bytes apart in the copy (32 more than a multiple of 128) and at other
+      // swizzle phases in the tile, so their 16-byte accesses meet no bank twice.
+      const int u = lane & 15, half = lane >> 4;      // (staging the query block)
       // the query block: see sparse attention's staging; rows are converted in
       // place to fp16, scaled by a power of two per row (exact), then moved to
       // tensor memory, thread (row, channel half) of two warps per quadrant
       auto stage_q = [&]() {
-        const uint32_t qsm = vs_s + (uint32_t)(qbuf * kVTile);
+        const uint32_t qsm = vs_s + (uint32_t)kVTile;
         const bool ok = wait_hot_warp(&sm.bar.q_ld, sph, abort_flag);
         if (ok) {
 #pragma unroll 1
-          for (int i0 = 0; i0 < 8; i0 += 2) {
+          for (int i0 = 0; i0 < (warp < 8 ? 8 : 0); i0 += 2) {
             uint4 a[2], c[2];
             uint32_t amax[2];
 #pragma unroll
@@ -473,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
               int ex2 = 0;
               const uint32_t eb = (amax[r] >> 7) & 0xffu;
               if (amax[r] != 0u && eb != 0xffu) ex2 = min(100, max(-100, 15 - ((int)eb - 126)));
-              const float up = __uint_as_float((uint32_t)(127 + ex2) << 23);
+              const float up = copysignf(__uint_as_float((uint32_t)(127 + ex2) << 23), p.softmax_scale);
               const uint32_t w[8] = {a[r].x, a[r].y, a[r].z, a[r].w,
                                      c[r].x, c[r].y, c[r].z, c[r].w};
               uint32_t f[8];
@@ -491,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
         bar_sync(kBarProducers, kProducers);
         const int h = quad * 16 + u;
 #pragma unroll 1
-        for (int i = 2 * (warp >> 2); i < 2 * (warp >> 2) + 2; ++i) {
+        for (int i = 2 * (warp >> 2); i < min(4, 2 * (warp >> 2) + 2); ++i) {
           uint32_t w[32];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -512,54 +508,72 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
         return ok;
       };
 
+      const int i4 = (lane >> 1) & 3, j8 = (lane >> 3) * 2 + (lane & 1);
+      // where the lane's 16-byte pieces go in a tile: chunk 4 (j % 2) + x of atom j / 2
+      uint32_t at[2][4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          at[k][x] = vs_s + (uint32_t)((j8 >> 1) * kAtom + swz(8 * warp + 4 * k + i4, 4 * (j8 & 1) + x));
+      const uint32_t row = smem_u32(raw) + (uint32_t)((8 * warp + i4) * kRowBytes + 16 * j8);
+      const uint32_t srow = smem_u32(raw) + (uint32_t)((8 * warp + i4) * kRowBytes + 256 + 2 * j8);
       bool ok = stage_q();
-      for (int t = 0; t < nt; ++t) {
-        const uint32_t g = g0 + t;
-        const int buf = (int)(g & 1);
-        const uint32_t ph = (g >> 1) & 1;
+      // one tile of buffer `buf` (a constant after inlining)
+      auto tile = [&](int t, int buf) {
+        const uint32_t ph = (used[buf] + (uint32_t)(t >> 1)) & 1;
+        uint4 code[2][2];            // [half][k]: 32 channels
+        uint32_t scale[2][2];        // their two scales
         bar_sync(kBarL + buf, kNumL);
         ok = ok && wait_hot_warp(&sm.bar.raw_full[buf], ph, abort_flag);
-        if (t >= 2) bar_sync(kBarF + buf, kNumF);
-        const uint32_t* valid = sm.valid[g & 3];
+        if (ok) {
+          const uint32_t o = (uint32_t)(buf * kRawTile);
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              code[hh][k] = lds128(row + o + 4 * k * kRowBytes + 128 * hh);
+              scale[hh][k] = lds16(srow + o + 4 * k * kRowBytes + 16 * hh);
+            }
+          const uint4 v = sm.valid[(g0 + t) & 3];
+          if (!((v.x & v.y) == ~0u && (v.z & 0xffffu) == 0xffffu)) {
+            const uint32_t w = warp < 4 ? v.x : warp < 8 ? v.y : v.z;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (!(w >> ((8 * warp + 4 * k + i4) & 31) & 1u)) {   // nothing was copied there
+                code[0][k] = code[1][k] = make_uint4(0, 0, 0, 0);
+                scale[0][k] = scale[1][k] = 0;
+              }
+          }
+        }
         // channels 0-255, then 256-511: each half is freed, filled and multiplied
         // on its own, so that S starts when half a tile is there
-#pragma unroll 1
-        for (int hh = 0; hh < 2; ++hh) {
-          // channels 256 hh + 16 u: atom 4 hh + u / 4, 16-byte chunks 2 (u % 4), + 1
-          const uint32_t a0 = vs_s + (uint32_t)(buf * kVTile + (4 * hh + (u >> 2)) * kAtom);
-          const uint32_t rows = smem_u32(raw) + (uint32_t)(buf * kRawTile);
-          uint2 c[kPerWarp / 2];
-          uint32_t sc[kPerWarp / 2];
-          if (ok) {
 #pragma unroll
-            for (int r = 0; r < kPerWarp / 2; ++r) {
-              const uint32_t row = rows + (uint32_t)((warp * kPerWarp + 2 * r + half) * kRowBytes);
-              c[r] = lds64(row + 128 * hh + 8 * u);
-              sc[r] = lds8(row + 256 + 16 * hh + u);
-            }
-          }
+        for (int hh = 0; hh < 2; ++hh) {
           ok = ok && wait_hot_warp(&sm.bar.v_free[buf][hh], ph ^ 1, abort_flag);
           if (ok) {
+            const uint32_t o = (uint32_t)(buf * kVTile + hh * 4 * kAtom);
 #pragma unroll
-            for (int r = 0; r < kPerWarp / 2; ++r) {
-              const int e = warp * kPerWarp + 2 * r + half;
-              if (!(valid[e >> 5] >> (e & 31) & 1u)) {      // nothing was copied there
-                c[r] = make_uint2(0, 0);
-                sc[r] = 0;
-              }
-              const __half2 f = e4m3x2_to_half2((uint16_t)(sc[r] * 0x0101u));
-              // lanes u and u + 4 would meet in one bank group: every other four
-              // take their two chunks in the other order
-              const int odd = (u >> 2) & 1, k = (u & 3) * 2 + odd;
-              sts128(a0 + swz(e, k), dq8(odd ? c[r].y : c[r].x, f));
-              sts128(a0 + swz(e, k ^ 1), dq8(odd ? c[r].x : c[r].y, f));
+            for (int k = 0; k < 2; ++k) {
+              const uint4 c = code[hh][k];
+              // byte 0 twice, byte 1 twice
+              const __half2 lo = e4m3x2_to_half2((uint16_t)__byte_perm(scale[hh][k], 0, 0x0000));
+              const __half2 hi = e4m3x2_to_half2((uint16_t)__byte_perm(scale[hh][k], 0, 0x1111));
+              sts128(at[k][0] + o, dq8(c.x, lo));
+              sts128(at[k][1] + o, dq8(c.y, lo));
+              sts128(at[k][2] + o, dq8(c.z, hi));
+              sts128(at[k][3] + o, dq8(c.w, hi));
             }
           }
           fence_async_smem();
           bar_arrive(kBarV + 2 * buf + hh, hh ? kNumV1 : kNumV0);
         }
+      };
+#pragma unroll 1
+      for (int t = 0; t < nt; t += 2) {
+        tile(t, 0);
+        if (t + 1 < nt) tile(t + 1, 1);
       }
-      for (int t = max(0, nt - 2); t < nt; ++t) bar_sync(kBarF + (int)((g0 + t) & 1), kNumF);
     } else if (warp == kLoadWarp) {
       // ---------------------------------------------------------- bulk copies
       // Lane i copies the rows of a tile that lie in its i-th page (a tile of 80
@@ -582,8 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
       };
       int place = fetch(0);
       for (int t = 0; t < nt; ++t) {
-        const uint32_t g = g0 + t;
-        const int buf = (int)(g & 1);
+        const int buf = t & 1;
         long long lo, hi;
         range(t, &lo, &hi);
         const int place_next = fetch(t + 1);
@@ -602,8 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
         }
         if (t >= 2) bar_sync(kBarV + 2 * buf + 1, kNumV1);     // the rows before are read
         if (lane == 0) {
-#pragma unroll
-          for (int w = 0; w < 3; ++w) sm.valid[g & 3][w] = bits[w];
+          sm.valid[(g0 + t) & 3] = make_uint4(bits[0], bits[1], bits[2], 0);
           mbar_arrive_expect_tx(&sm.bar.raw_full[buf],
                                 (uint32_t)(__popc(bits[0]) + __popc(bits[1]) + __popc(bits[2])) *
                                     kRowBytes);
@@ -617,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
         place = place_next;
       }
       for (int t = max(0, nt - 2); t < nt; ++t)
-        bar_sync(kBarV + 2 * (int)((g0 + t) & 1) + 1, kNumV1);
+        bar_sync(kBarV + 2 * (t & 1) + 1, kNumV1);
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMA issuer
       // The whole warp runs this with warp-uniform values and one elected lane
@@ -630,7 +642,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
       const uint64_t p0 = desc_sw128(ps_s, 16, 1024);       // P as K-major A
       const uint64_t p1 = desc_sw32(ps_s + 2 * kP0);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint32_t gu = __shfl_sync(0xffffffffu, g0, 0);
       const int ntu = __shfl_sync(0xffffffffu, nt, 0);
       bar_sync(kBarQ, kNumQ);
       auto issue_s = [&](uint32_t buf, int hh) {
@@ -663,12 +674,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
         }
         __syncwarp();
       };
+      bool go = true;
       for (int t = 0; t < ntu; t += 2) {
         const int more = min(2, ntu - t);
-        const bool go = !__any_sync(0xffffffffu, *abort_flag != 0);
 #pragma unroll 1
         for (int i = 0; i < more; ++i) {
-          const uint32_t buf = (gu + t + i) & 1;
+          const uint32_t buf = (uint32_t)i;      // t is even
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             bar_sync(kBarV + 2 * buf + hh, hh ? kNumV1 : kNumV0);
@@ -676,12 +687,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
           }
           bar_arrive(kBarS + buf, kNumS);
         }
+        go = !__any_sync(0xffffffffu, *abort_flag != 0);
 #pragma unroll 1
         for (int i = 0; i < more; ++i) {
-          const uint32_t buf = (gu + t + i) & 1;
+          const uint32_t buf = (uint32_t)i;      // t is even
           bar_sync(kBarP + buf, kNumP);
           if (go) issue_pv(buf, t + i > 0 ? 1u : 0u);
-          bar_arrive(kBarF + buf, kNumF);
         }
       }
       if (elect_one()) mma_commit(&sm.bar.o_full);
@@ -694,24 +705,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
       const int h = quad * 16 + hl;
       bar_sync(kBarQ, kNumQ);
       const bool real = h < nr;
-      const float hs = real ? p.softmax_scale * kLog2e * sm.qdown[h] : 0.0f;
+      const float hs = real ? fabsf(p.softmax_scale) * kLog2e * sm.qdown[h] : 0.0f;
       // entries that this row sees
       const int n_row = real ? (p.nvalid ? visible(p, b, (r0 + h) / p.Hq, false) : n_most) : n_most;
       bool ok = true;
       for (int t = 0; t < nt; ++t) {
-        const uint32_t g = g0 + t;
-        const int buf = (int)(g & 1);
+        const int buf = t & 1;
         bar_sync(kBarS + buf, kNumS);
-        ok = ok && wait_hot_warp(&sm.bar.s_full[buf], (g >> 1) & 1, abort_flag);
+        ok = ok && wait_hot_warp(&sm.bar.s_full[buf], (used[buf] + (uint32_t)(t >> 1)) & 1, abort_flag);
         if (ok) {
           tc_fence_after();
           // this thread's entries: 40 ch .. + 39 of the tile, masks of 32 and 8
           const int left = n_row - (t0 + t) * kT - kHalfT * ch;
           uint32_t m0, m1;
           {
-            const uint32_t* v = sm.valid[g & 3];
-            m0 = ch ? (v[1] >> 8) | (v[2] << 24) : v[0];
-            m1 = (ch ? v[2] >> 8 : v[1]) & 0xffu;
+            const uint4 v = sm.valid[(g0 + t) & 3];
+            m0 = ch ? (v.y >> 8) | (v.z << 24) : v.x;
+            m1 = (ch ? v.z >> 8 : v.y) & 0xffu;
             if (left < kHalfT) {
               m0 &= left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1u;
               m1 &= left <= 32 ? 0u : (1u << (left - 32)) - 1u;
@@ -719,22 +729,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
           }
           float y[kHalfT];
           tmem_ld_logits(tmem + lanes + (uint32_t)kT * buf, y);
+          // (the scale is not negative: its sign went into the query block)
           float xmax = -INFINITY;
-          if (__all_sync(0xffffffffu, m0 == ~0u && m1 == 0xffu)) {
+          const bool all = __all_sync(0xffffffffu, m0 == ~0u && m1 == 0xffu) != 0;
+          if (all) {
 #pragma unroll
-            for (int j = 0; j < kHalfT; ++j) {
-              y[j] *= hs;
-              xmax = fmaxf(xmax, y[j]);
-            }
+            for (int j = 0; j < kHalfT; ++j) xmax = fmaxf(xmax, y[j]);
           } else {
 #pragma unroll
-            for (int j = 0; j < kHalfT; ++j) {
-              const bool there = ((j < 32 ? m0 >> j : m1 >> (j - 32)) & 1u) != 0u;
-              y[j] = there ? y[j] * hs : -INFINITY;
-              xmax = fmaxf(xmax, y[j]);
-            }
+            for (int j = 0; j < kHalfT; ++j)
+              if ((j < 32 ? m0 >> j : m1 >> (j - 32)) & 1u) xmax = fmaxf(xmax, y[j]);
           }
           xmax = fmaxf(xmax, __shfl_xor_sync(0xffffffffu, xmax, 16));
+          if (xmax != -INFINITY) xmax *= hs;
           const bool raise = xmax > m_ref + kRescaleSlack;
           if (__any_sync(0xffffffffu, raise)) {
             float alpha = 1.0f;
@@ -746,8 +753,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
             // O holds the tiles before: rescaled once they are complete (O += of
             // this one waits for its P)
             if (t > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-              const uint32_t gb = g - 1;
-              ok = wait_hot_warp(&sm.bar.v_free[gb & 1][1], (gb >> 1) & 1, abort_flag);
+              const int pb = buf ^ 1;
+              ok = wait_hot_warp(&sm.bar.v_free[pb][1], (used[pb] + (uint32_t)((t - 1) >> 1)) & 1,
+                                 abort_flag);
               if (ok) {
                 tc_fence_after();
 #pragma unroll 1
@@ -768,8 +776,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float x0 = fast_exp2(y[8 * k + 2 * i] - mm);
-              const float x1 = fast_exp2(y[8 * k + 2 * i + 1] - mm);
+              const int j = 8 * k + 2 * i;
+              float x0 = fast_exp2(fmaf(y[j], hs, -mm)), x1 = fast_exp2(fmaf(y[j + 1], hs, -mm));
+              if (!all) {
+                if (!((j < 32 ? m0 >> j : m1 >> (j - 32)) & 1u)) x0 = 0.0f;
+                if (!((j + 1 < 32 ? m0 >> (j + 1) : m1 >> (j + 1 - 32)) & 1u)) x1 = 0.0f;
+              }
               l += x0 + x1;
               w[i] = pack_half2(x0, x1);
             }
@@ -791,7 +803,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
 
     // -------------------------------------------------------------- output
     bool have_o = false;
-    if (warp != kMmaWarp && warp != kLoadWarp) have_o = mbar_wait_warp(&sm.bar.o_full, sph, abort_flag);
+    const bool softmaxer = warp >= kProducerWarps;
+    if (warp < 8 || (softmaxer && warp < kMmaWarp)) have_o = mbar_wait_warp(&sm.bar.o_full, sph, abort_flag);
     tc_fence_before();
     __syncthreads();                  // O^T is final, the (maximum, sum) pairs are in place
     tc_fence_after();
@@ -800,8 +813,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
       const float2 ml = sm.mlf[h];
       // chunks of 32 columns (and the same 256 further): the quadrant's softmax
       // warp takes 0-2, its producer warps 3-5 and 6-7
-      const int cb = warp > kMmaWarp ? 0 : warp < 4 ? 3 : 6;
-      const int ce = warp > kMmaWarp ? 3 : warp < 4 ? 6 : 8;
+      const int cb = softmaxer ? 0 : warp < 4 ? 3 : 6;
+      const int ce = softmaxer ? 3 : warp < 4 ? 6 : 8;
 #pragma unroll 1
       for (int c = cb; c < ce; ++c) {
         float o[32];
@@ -825,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
             dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
       }
-      if (warp > kMmaWarp && ch == 0 && h < nr) {
+      if (softmaxer && ch == 0 && h < nr) {
         if (!whole)
           p.ws_ml[(size_t)slot * kRows + h] = ml;
         else if (p.lse)
@@ -837,6 +850,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
     tc_fence_after();
     if (stop) break;
     g0 += (uint32_t)nt;
+    used[0] += (uint32_t)(nt + 1) / 2;
+    used[1] += (uint32_t)nt / 2;
     pos += nt;
     if (pos == seq_base + (long long)p.nblk * tiles) {
       seq_base = pos;
