@@ -82,13 +82,24 @@ struct __align__(8) Bars {
   uint64_t q_ld, o_full, s_full[2], raw_full[2], v_free[2][2];   // v_free: [tile][half]
 };
 
+// A segment of a CTA's piece: tiles [t0, t0 + nt) of row block blk of sequence b.
+// (In shared memory, so that no role holds it in registers through its loop.)
+struct Segment {
+  int b, blk, t0, nt;        // nt 0: there is none
+  int n_most;                // entries that the sequence's queries see at most
+  int tiles;
+  int slot;                  // where its partial goes, -1: it is whole
+  uint32_t g0, used0, used1; // tiles of this CTA before it, in all and by buffer
+};
+
 struct __align__(16) Smem {
   Bars bar;
+  Segment seg[2];
   uint32_t tmem_slot;
   int abort_flag;
-  long long base;                   // tiles before the first sequence of this piece
   long long total;                  // tiles in all
-  int first_b;
+  long long pos, end;               // this piece's tiles not yet in a segment
+  long long base;                   // tiles before the sequence that pos lies in
   uint4 valid[4];                   // bit i of a tile's 128: entry i is there
   float2 mlf[kRows];                // (reference maximum, row sum)
   float qdown[kRows];               // the power of two each row was scaled up by, inverted
@@ -316,7 +327,41 @@ __device__ __forceinline__ int piece_of(long long tile, int pieces, long long to
   return (int)(((tile + 1) * pieces - 1) / total);
 }
 
-__global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params p) {
+// Cuts the next segment off the piece: sm.seg[at] from its predecessor
+// sm.seg[at ^ 1] (whose b, or the one after it, is the sequence at sm.pos). One thread.
+__device__ __noinline__ void next_segment(const Params& p, Smem& sm, int at) {
+  const Segment& prev = sm.seg[at ^ 1];
+  Segment s;
+  s.g0 = prev.g0 + (uint32_t)prev.nt;
+  s.used0 = prev.used0 + (uint32_t)(prev.nt + 1) / 2;
+  s.used1 = prev.used1 + (uint32_t)prev.nt / 2;
+  s.b = prev.b;
+  s.nt = 0;
+  s.blk = s.t0 = s.n_most = s.tiles = s.slot = 0;
+  const long long pos = sm.pos;
+  if (pos < sm.end) {
+    if (prev.nt > 0 && pos == sm.base + (long long)p.nblk * prev.tiles) {
+      sm.base = pos;
+      ++s.b;
+    }
+    const int pieces = (int)min((long long)gridDim.x, sm.total), piece = (int)blockIdx.x;
+    s.n_most = visible_most(p, s.b, false);
+    s.tiles = tiles_of(s.n_most);
+    s.blk = (int)((pos - sm.base) / s.tiles);
+    const long long pair = sm.base + (long long)s.blk * s.tiles;
+    s.t0 = (int)(pos - pair);
+    s.nt = (int)min((long long)(s.tiles - s.t0), sm.end - pos);
+    const int slot = 2 * piece + (pos == piece_begin(piece, pieces, sm.total) ? 0 : 1);
+    s.slot = s.nt == s.tiles ? -1 : slot;
+    if (s.t0 == 0)
+      p.ws_info[(size_t)s.b * p.nblk + s.blk] =
+          make_int4(piece, piece_of(pair + s.tiles - 1, pieces, sm.total), slot, 0);
+    sm.pos = pos + s.nt;
+  }
+  sm.seg[at] = s;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t vs[];   // [2][8 atoms][80 entries][128 B]
   uint8_t* ps = vs + 2 * kVTile;               // [2][64 rows][128 B], [2][64 rows][32 B]
   uint8_t* raw = ps + 2 * (kP0 + kP1);         // [2][80 entries][288 B]
@@ -353,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
     __syncthreads();
     if (threadIdx.x < 32) {
       long long run = 0;
-      for (int i = lane; i < kThreads; i += 32) {
+      for (int i = lane; i - lane < (p.B + each - 1) / each; i += 32) {
         const long long x = sums[i];
         long long incl = x;
 #pragma unroll
@@ -374,58 +419,39 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
     if (begin >= before && begin < before + mine) {
       long long at = before;
       int b = b0;
-      for (;; ++b) {
+      for (; b + 1 < b1; ++b) {
         const long long k = (long long)p.nblk * tiles_of(visible_most(p, b, false));
         if (begin < at + k) break;
         at += k;
       }
-      sm.first_b = b;
+      sm.seg[1].b = b;
       sm.base = at;
+      sm.seg[1].nt = 0;
+      sm.seg[1].g0 = sm.seg[1].used0 = sm.seg[1].used1 = 0;
+      sm.pos = begin;
+      sm.end = (int)blockIdx.x < pieces ? piece_begin((int)blockIdx.x + 1, pieces, total) : begin;
+      next_segment(p, sm, 0);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_slot;
-  const long long total = sm.total;
-  const int pieces = (int)min((long long)gridDim.x, total);
-  const int piece = blockIdx.x;
-  long long pos = piece < pieces ? piece_begin(piece, pieces, total) : 0;
-  const long long end = piece < pieces ? piece_begin(piece + 1, pieces, total) : 0;
-  long long seq_base = sm.base;
-  int b = sm.first_b;
-
-  const uint32_t vs_s = smem_u32(vs), ps_s = smem_u32(ps);   // 1024-byte aligned, as swizzles need
+  const uint32_t vs_s = smem_u32(vs), ps_s = smem_u32(ps);
   const int quad = warp & 3;
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-  uint32_t g0 = 0;                  // tiles of this CTA before the current segment
-  uint32_t used[2] = {0, 0};        // ... by buffer (a segment starts with buffer 0)
-  const long long piece_first = pos;
 
-  for (uint32_t sg = 0; pos < end; ++sg) {
-    // ---- the next segment: tiles [t0, t1) of (b, blk)
-    const int n_most = visible_most(p, b, false);
-    const int tiles = tiles_of(n_most);
-    const int blk = (int)((pos - seq_base) / tiles);
-    const long long pair_base = seq_base + (long long)blk * tiles;
-    const int t0 = (int)(pos - pair_base);
-    const int nt = (int)min((long long)(tiles - t0), end - pos);
-    const bool whole = nt == tiles;
-    const int slot = 2 * piece + (pos == piece_first ? 0 : 1);
-    const int r0 = blk * kRows;                            // first query row of the block
-    const int nr = min(kRows, p.Tq * p.Hq - r0);
-    const size_t row0 = (size_t)b * p.Tq * p.Hq + r0;
+  for (uint32_t sg = 0; sm.seg[sg & 1].nt > 0; ++sg) {
+    const Segment& S = sm.seg[sg & 1];
     const uint32_t sph = sg & 1;                           // phase of the per-segment barriers
+    const int nt = S.nt;
     if (threadIdx.x == 0) {
-      if (t0 == 0) {
-        const int first = piece, last = piece_of(pair_base + tiles - 1, pieces, total);
-        p.ws_info[(size_t)b * p.nblk + blk] = make_int4(first, last, slot, 0);
-      }
-      const uint32_t qbytes = (uint32_t)nr * kD * 2;
+      const int r0 = S.blk * kRows;
+      const uint32_t qbytes = (uint32_t)min(kRows, p.Tq * p.Hq - r0) * kD * 2;
       mbar_arrive_expect_tx(&sm.bar.q_ld, qbytes);
-      bulk_load(vs + kVTile, p.q + row0 * kD, qbytes, &sm.bar.q_ld);   // the second tile, for now
+      bulk_load(vs + kVTile, p.q + ((size_t)S.b * p.Tq * p.Hq + r0) * kD, qbytes,
+                &sm.bar.q_ld);                             // the second tile, for now
     }
-    float m_ref = -INFINITY, l = 0.0f;
 
     if (warp < kProducerWarps) {
       // ---------------------------------------------------------- load + dequantise
@@ -438,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
       // the query block: see sparse attention's staging; rows are converted in
       // place to fp16, scaled by a power of two per row (exact), then moved to
       // tensor memory, thread (row, channel half) of two warps per quadrant
+      const int nr = min(kRows, p.Tq * p.Hq - S.blk * kRows);
       auto stage_q = [&]() {
         const uint32_t qsm = vs_s + (uint32_t)kVTile;
         const bool ok = wait_hot_warp(&sm.bar.q_ld, sph, abort_flag);
@@ -519,9 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
       const uint32_t row = smem_u32(raw) + (uint32_t)((8 * warp + i4) * kRowBytes + 16 * j8);
       const uint32_t srow = smem_u32(raw) + (uint32_t)((8 * warp + i4) * kRowBytes + 256 + 2 * j8);
       bool ok = stage_q();
+      const uint32_t g0 = S.g0, used0 = S.used0, used1 = S.used1;
       // one tile of buffer `buf` (a constant after inlining)
       auto tile = [&](int t, int buf) {
-        const uint32_t ph = (used[buf] + (uint32_t)(t >> 1)) & 1;
+        const uint32_t ph = ((buf ? used1 : used0) + (uint32_t)(t >> 1)) & 1;
         uint4 code[2][2];            // [half][k]: 32 channels
         uint32_t scale[2][2];        // their two scales
         bar_sync(kBarL + buf, kNumL);
@@ -578,8 +606,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
       // ---------------------------------------------------------- bulk copies
       // Lane i copies the rows of a tile that lie in its i-th page (a tile of 80
       // entries touches at most 11 pages of 8).
-      const int s = p.seq ? __ldg(p.seq + b) : b;
-      const int32_t* table = p.pg.table + (size_t)(n_most > 0 ? s : 0) * p.pg.M;
+      const int n_most = S.n_most, t0 = S.t0;
+      const uint32_t g0 = S.g0;
+      const int s = n_most > 0 ? (p.seq ? __ldg(p.seq + S.b) : S.b) : 0;
+      const int32_t* table = p.pg.table + (size_t)s * p.pg.M;
       // entries [lo, hi) of the sequence in lane i's page of tile t
       auto range = [&](int t, long long* lo, long long* hi) {
         const long long e0 = (long long)(t0 + t) * kT;
@@ -630,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
       }
       for (int t = max(0, nt - 2); t < nt; ++t)
         bar_sync(kBarV + 2 * (t & 1) + 1, kNumV1);
+      if (lane == 0) next_segment(p, sm, (int)(sph ^ 1));
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMA issuer
       // The whole warp runs this with warp-uniform values and one elected lane
@@ -704,19 +735,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
       const int hl = lane & 15, ch = lane >> 4;
       const int h = quad * 16 + hl;
       bar_sync(kBarQ, kNumQ);
-      const bool real = h < nr;
+      const int r0 = S.blk * kRows;
+      const bool real = r0 + h < p.Tq * p.Hq;
       const float hs = real ? fabsf(p.softmax_scale) * kLog2e * sm.qdown[h] : 0.0f;
-      // entries that this row sees
-      const int n_row = real ? (p.nvalid ? visible(p, b, (r0 + h) / p.Hq, false) : n_most) : n_most;
+      // entries that this row sees from the segment's first on
+      const int n_row = (real && p.nvalid ? visible(p, S.b, (r0 + h) / p.Hq, false) : S.n_most) - S.t0 * kT;
+      const uint32_t g0 = S.g0, used0 = S.used0, used1 = S.used1;
+      float m_ref = -INFINITY, l = 0.0f;
       bool ok = true;
       for (int t = 0; t < nt; ++t) {
         const int buf = t & 1;
         bar_sync(kBarS + buf, kNumS);
-        ok = ok && wait_hot_warp(&sm.bar.s_full[buf], (used[buf] + (uint32_t)(t >> 1)) & 1, abort_flag);
+        ok = ok && wait_hot_warp(&sm.bar.s_full[buf], ((buf ? used1 : used0) + (uint32_t)(t >> 1)) & 1, abort_flag);
         if (ok) {
           tc_fence_after();
           // this thread's entries: 40 ch .. + 39 of the tile, masks of 32 and 8
-          const int left = n_row - (t0 + t) * kT - kHalfT * ch;
+          const int left = n_row - t * kT - kHalfT * ch;
           uint32_t m0, m1;
           {
             const uint4 v = sm.valid[(g0 + t) & 3];
@@ -730,16 +764,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
           float y[kHalfT];
           tmem_ld_logits(tmem + lanes + (uint32_t)kT * buf, y);
           // (the scale is not negative: its sign went into the query block)
-          float xmax = -INFINITY;
+          float xm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           const bool all = __all_sync(0xffffffffu, m0 == ~0u && m1 == 0xffu) != 0;
           if (all) {
 #pragma unroll
-            for (int j = 0; j < kHalfT; ++j) xmax = fmaxf(xmax, y[j]);
+            for (int j = 0; j < kHalfT; ++j) xm[j & 3] = fmaxf(xm[j & 3], y[j]);
           } else {
 #pragma unroll
             for (int j = 0; j < kHalfT; ++j)
-              if ((j < 32 ? m0 >> j : m1 >> (j - 32)) & 1u) xmax = fmaxf(xmax, y[j]);
+              if ((j < 32 ? m0 >> j : m1 >> (j - 32)) & 1u) xm[j & 3] = fmaxf(xm[j & 3], y[j]);
           }
+          float xmax = fmaxf(fmaxf(xm[0], xm[1]), fmaxf(xm[2], xm[3]));
           xmax = fmaxf(xmax, __shfl_xor_sync(0xffffffffu, xmax, 16));
           if (xmax != -INFINITY) xmax *= hs;
           const bool raise = xmax > m_ref + kRescaleSlack;
@@ -754,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
             // this one waits for its P)
             if (t > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
               const int pb = buf ^ 1;
-              ok = wait_hot_warp(&sm.bar.v_free[pb][1], (used[pb] + (uint32_t)((t - 1) >> 1)) & 1,
+              ok = wait_hot_warp(&sm.bar.v_free[pb][1], ((pb ? used1 : used0) + (uint32_t)((t - 1) >> 1)) & 1,
                                  abort_flag);
               if (ok) {
                 tc_fence_after();
@@ -771,6 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
             }
           }
           const float mm = m_ref == -INFINITY ? 0.0f : m_ref;   // nothing seen yet: 2^-inf = 0
+          float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int k = 0; k < kHalfT / 8; ++k) {
             uint32_t w[4];
@@ -782,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
                 if (!((j < 32 ? m0 >> j : m1 >> (j - 32)) & 1u)) x0 = 0.0f;
                 if (!((j + 1 < 32 ? m0 >> (j + 1) : m1 >> (j + 1 - 32)) & 1u)) x1 = 0.0f;
               }
-              l += x0 + x1;
+              ls[i] += x0 + x1;
               w[i] = pack_half2(x0, x1);
             }
             const int c = (kHalfT / 8) * ch + k;      // 16-byte chunk: entries 8 c .. + 7
@@ -792,6 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
                                           (((c - 8) ^ (h >> 2 & 1)) << 4));
             sts128(at, make_uint4(w[0], w[1], w[2], w[3]));
           }
+          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
           fence_async_smem();
           tc_fence_before();
         }
@@ -802,61 +839,69 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
     }
 
     // -------------------------------------------------------------- output
-    bool have_o = false;
-    const bool softmaxer = warp >= kProducerWarps;
-    if (warp < 8 || (softmaxer && warp < kMmaWarp)) have_o = mbar_wait_warp(&sm.bar.o_full, sph, abort_flag);
-    tc_fence_before();
-    __syncthreads();                  // O^T is final, the (maximum, sum) pairs are in place
-    tc_fence_after();
-    if (have_o) {
-      const int hl = lane & 15, ch = lane >> 4, h = quad * 16 + hl;
-      const float2 ml = sm.mlf[h];
-      // chunks of 32 columns (and the same 256 further): the quadrant's softmax
-      // warp takes 0-2, its producer warps 3-5 and 6-7
-      const int cb = softmaxer ? 0 : warp < 4 ? 3 : 6;
-      const int ce = softmaxer ? 3 : warp < 4 ? 6 : 8;
+    // O through shared memory (the idle tiles), so that rows are written whole:
+    // [64 rows][2 KB], 16-byte chunk c of row h at c ^ (h & 7).
+    const bool softmaxer = warp >= kProducerWarps && warp < kMmaWarp;
+    if (warp < 8 || softmaxer) {
+      const bool have_o = wait_hot_warp(&sm.bar.o_full, sph, abort_flag);
+      tc_fence_after();
+      if (have_o) {
+        const int h = quad * 16 + (lane & 15), ch = lane >> 4;
+        // chunks of 32 columns (and the same 256 further): the quadrant's softmax
+        // warp takes 0-2, its producer warps 3-5 and 6-7
+        const int cb = softmaxer ? 0 : warp < 4 ? 3 : 6;
+        const int ce = softmaxer ? 3 : warp < 4 ? 6 : 8;
 #pragma unroll 1
-      for (int c = cb; c < ce; ++c) {
-        float o[32];
-        tmem_ld16x2_32<256>(tmem + lanes + kHalfLanes + 32u * c, o);
-        if (h >= nr) continue;
-        const int d0 = 256 * ch + 32 * c;           // this thread's channels d0 .. + 31
-        // (a row that saw nothing has sum 0 and zeros in O)
-        if (whole) {
-          const float f = ml.y > 0.0f ? 1.0f / ml.y : 0.0f;
-          uint4* dst = reinterpret_cast<uint4*>(p.out + (row0 + h) * kD + d0);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[k] = make_uint4(pack_bf162(o[8 * k] * f, o[8 * k + 1] * f),
-                                pack_bf162(o[8 * k + 2] * f, o[8 * k + 3] * f),
-                                pack_bf162(o[8 * k + 4] * f, o[8 * k + 5] * f),
-                                pack_bf162(o[8 * k + 6] * f, o[8 * k + 7] * f));
-        } else {
-          float4* dst = reinterpret_cast<float4*>(p.ws_o + ((size_t)slot * kRows + h) * kD + d0);
+        for (int c = cb; c < ce; ++c) {
+          float o[32];
+          tmem_ld16x2_32<256>(tmem + lanes + kHalfLanes + 32u * c, o);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            sts128(vs_s + (uint32_t)(h * 2048 + (((64 * ch + 8 * c + k) ^ (h & 7)) << 4)),
+                   make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
+                              __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3])));
         }
-      }
-      if (softmaxer && ch == 0 && h < nr) {
-        if (!whole)
-          p.ws_ml[(size_t)slot * kRows + h] = ml;
-        else if (p.lse)
-          p.lse[row0 + h] = ml.y > 0.0f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
       }
     }
     tc_fence_before();
     const bool stop = __syncthreads_or(*abort_flag) != 0;
     tc_fence_after();
     if (stop) break;
-    g0 += (uint32_t)nt;
-    used[0] += (uint32_t)(nt + 1) / 2;
-    used[1] += (uint32_t)nt / 2;
-    pos += nt;
-    if (pos == seq_base + (long long)p.nblk * tiles) {
-      seq_base = pos;
-      ++b;
+    {
+      const int r0 = S.blk * kRows, slot = S.slot;
+      const int nr = min(kRows, p.Tq * p.Hq - r0);
+      const size_t row0 = (size_t)S.b * p.Tq * p.Hq + r0;
+#pragma unroll 1
+      for (int h = warp; h < nr; h += kThreads / 32) {
+        const float2 ml = sm.mlf[h];
+        const uint32_t row = vs_s + (uint32_t)(h * 2048);
+        if (slot < 0) {
+          // (a row that saw nothing has sum 0 and zeros in O)
+          const float f = ml.y > 0.0f ? 1.0f / ml.y : 0.0f;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int c = 64 * k + 2 * lane;
+            const uint4 a = lds128(row + ((c ^ (h & 7)) << 4));
+            const uint4 d = lds128(row + (((c + 1) ^ (h & 7)) << 4));
+            reinterpret_cast<uint4*>(p.out + (row0 + h) * kD)[32 * k + lane] =
+                make_uint4(pack_bf162(__uint_as_float(a.x) * f, __uint_as_float(a.y) * f),
+                           pack_bf162(__uint_as_float(a.z) * f, __uint_as_float(a.w) * f),
+                           pack_bf162(__uint_as_float(d.x) * f, __uint_as_float(d.y) * f),
+                           pack_bf162(__uint_as_float(d.z) * f, __uint_as_float(d.w) * f));
+          }
+          if (p.lse && lane == 0)
+            p.lse[row0 + h] = ml.y > 0.0f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.ws_o + ((size_t)slot * kRows + h) * kD);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            dst[32 * k + lane] = lds128(row + (((32 * k + lane) ^ (h & 7)) << 4));
+          if (lane == 0) p.ws_ml[(size_t)slot * kRows + h] = ml;
+        }
+      }
     }
+    fence_async_smem();               // the tiles are next written by a bulk copy
+    __syncthreads();
   }
   tc_fence_before();
   __syncthreads();
@@ -868,7 +913,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const Params
 }
 
 // Joins the pieces of one query row: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
-__global__ void __launch_bounds__(128) paged_combine_kernel(const Params p) {
+// 128 threads hold the row's channels, four groups of them take every fourth piece
+// (one group took 14 us for rows of 37 pieces: a chain of loads).
+constexpr int kCombineGroups = 4;
+
+__global__ void __launch_bounds__(128 * kCombineGroups) paged_combine_kernel(const Params p) {
+  __shared__ float4 part[kCombineGroups][128];
+  __shared__ float part_l[kCombineGroups];
   pdl_wait_and_release();
   const int per_seq = p.Tq * p.Hq;
   const int r = blockIdx.x;                            // row of the sequence
@@ -876,18 +927,20 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const Params p) {
   const int4 info = p.ws_info[b * p.nblk + r / kRows];
   const int first = info.x, last = info.y;
   if (first == last) return;
-  const int h = r % kRows;
+  const int h = r % kRows, lane = threadIdx.x & 31;
+  const int grp = threadIdx.x >> 7, d4 = threadIdx.x & 127;
   auto slot_of = [&](int i) { return (size_t)(i == first ? info.z : 2 * i) * kRows + h; };
   float M = -INFINITY;
-  for (int i = first; i <= last; ++i) M = fmaxf(M, p.ws_ml[slot_of(i)].x);
+  for (int i = first + lane; i <= last; i += 32) M = fmaxf(M, p.ws_ml[slot_of(i)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float L = 0.0f;
   float4 acc = make_float4(0, 0, 0, 0);
-  const int d = threadIdx.x * 4;
   if (M != -INFINITY) {
 #pragma unroll 4
-    for (int i = first; i <= last; ++i) {
+    for (int i = first + grp; i <= last; i += kCombineGroups) {
       const float2 ml = p.ws_ml[slot_of(i)];
-      const float4 v = *reinterpret_cast<const float4*>(p.ws_o + slot_of(i) * kD + d);
+      const float4 v = *reinterpret_cast<const float4*>(p.ws_o + slot_of(i) * kD + 4 * d4);
       const float w = exp2f(ml.x - M);                 // 0 for a piece that saw nothing
       L = fmaf(w, ml.y, L);
       acc.x = fmaf(w, v.x, acc.x);
@@ -896,12 +949,23 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const Params p) {
       acc.w = fmaf(w, v.w, acc.w);
     }
   }
+  part[grp][d4] = acc;
+  if (d4 == 0) part_l[grp] = L;
+  __syncthreads();
+  if (grp > 0) return;
+#pragma unroll
+  for (int k = 1; k < kCombineGroups; ++k) {
+    const float4 v = part[k][d4];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+    L += part_l[k];
+  }
   const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   const size_t row = b * per_seq + r;
-  *reinterpret_cast<uint2*>(p.out + row * kD + d) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  *reinterpret_cast<uint2*>(p.out + row * kD + 4 * d4) =
+      make_uint2(pack_bf162(acc.x * inv, acc.y * inv), pack_bf162(acc.z * inv, acc.w * inv));
   if (p.lse && threadIdx.x == 0) p.lse[row] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
@@ -964,7 +1028,8 @@ cudaError_t launch_paged_attn_dense(const uint16_t* q, const fp4_kv_pages& pg, c
   e = launch_pdl(paged_attn_tc_kernel, dim3(pieces), dim3(kThreads), kSmemBytes, stream, dim3(1),
                  p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_combine_kernel, dim3(Tq * Hq, B), dim3(128), 0, stream, dim3(1), p);
+  return launch_pdl(paged_combine_kernel, dim3(Tq * Hq, B),
+                    dim3(128 * kCombineGroups), 0, stream, dim3(1), p);
 }
 
 }  // namespace csa2
