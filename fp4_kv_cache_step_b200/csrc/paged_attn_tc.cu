@@ -15,7 +15,7 @@
 // Work is dealt out by tiles: the tiles of all (sequence, row block) pairs stand in
 // one line that is cut into as many equal pieces as there are SMs, so a ragged
 // batch keeps every SM busy. A pair that lies within one piece is written out;
-// one that is cut leaves fp32 partials with their (maximum, sum), which
+// one that is cut leaves fp16 partials with their (maximum, sum), which
 // paged_combine_kernel joins. A sequence without entries has one empty tile.
 //
 // Roles. Warp 15 copies rows (288 bytes each, contiguous within a page) to shared
@@ -32,6 +32,8 @@
 // 800; what the tensor core or the copy engine signals are mbarriers, every wait
 // on one of which is bounded. Named barriers need no bound: each role passes every
 // one of them for every tile, whether or not a wait before it ran out.
+#include <mutex>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -118,7 +120,7 @@ struct Params {
   float softmax_scale;
   uint16_t* out;
   float* lse;
-  float* ws_o;        // [slot][64][512]
+  __half* ws_o;       // [slot][64][512]: partial outputs, each over its own row sum
   float2* ws_ml;      // [slot][64]
   int4* ws_info;      // [B][nblk]: first and last piece, the first one's slot
   int* err;
@@ -297,39 +299,59 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) {
 }
 
 // ---------------------------------------------------------------- lengths, pieces
-// Visible entries of query (b, t): nvalid, or the slot's length.
-__device__ int visible(const Params& p, int b, int t, bool tell) {
+// Entries that slot seq[b] holds (0 for a bad slot).
+__device__ __forceinline__ int slot_len(const Params& p, int b, bool tell) {
   const int s = p.seq ? __ldg(p.seq + b) : b;
   if (s < 0 || s >= p.pg.S) {
     if (tell) record_error(p.err, CSA2_ERR_DEVICE_INDEX);
     return 0;
   }
-  const int len = min(max(0, __ldg(p.pg.len + s)), p.pg.M << p.shift);
-  if (p.nvalid == nullptr) return len;
-  const int n = __ldg(p.nvalid + (size_t)b * p.Tq + t);
-  if (tell && (n < 0 || n > len)) record_error(p.err, CSA2_ERR_DEVICE_INDEX);
-  return min(max(0, n), len);
+  return min(max(0, __ldg(p.pg.len + s)), p.pg.M << p.shift);
 }
 
+// Entries that query (b, t) sees: nvalid within [0, len], or len.
+__device__ int visible(const Params& p, int b, int t) {
+  const int len = slot_len(p, b, false);
+  return p.nvalid ? min(max(0, __ldg(p.nvalid + (size_t)b * p.Tq + t)), len) : len;
+}
+
+// ... that its queries see at most.
 __device__ int visible_most(const Params& p, int b, bool tell) {
-  int n = 0;
-  for (int t = 0; t < (p.nvalid ? p.Tq : 1); ++t) n = max(n, visible(p, b, t, tell));
-  return n;
+  int lo = 0, hi = 0;
+  if (p.nvalid) {
+    const int32_t* n = p.nvalid + (size_t)b * p.Tq;
+    lo = hi = __ldg(n);
+#pragma unroll 4
+    for (int t = 1; t < p.Tq; ++t) {
+      const int x = __ldg(n + t);
+      lo = min(lo, x);
+      hi = max(hi, x);
+    }
+  }
+  const int len = slot_len(p, b, tell);
+  if (!p.nvalid) return len;
+  if (tell && (lo < 0 || hi > len)) record_error(p.err, CSA2_ERR_DEVICE_INDEX);
+  return min(max(0, hi), len);
 }
 
 __device__ __forceinline__ int tiles_of(int n) { return max(1, (n + kT - 1) / kT); }
 
+// a / b for a >= 0, b > 0 (the 32-bit division is several times shorter)
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // Piece i of `pieces` holds the tiles [piece_begin(i), piece_begin(i + 1)) of `total`.
 __device__ __forceinline__ long long piece_begin(int i, int pieces, long long total) {
-  return (long long)i * total / pieces;
+  return quotient((long long)i * total, pieces);
 }
 __device__ __forceinline__ int piece_of(long long tile, int pieces, long long total) {
-  return (int)(((tile + 1) * pieces - 1) / total);
+  return (int)quotient((tile + 1) * pieces - 1, total);
 }
 
 // Cuts the next segment off the piece: sm.seg[at] from its predecessor
-// sm.seg[at ^ 1] (whose b, or the one after it, is the sequence at sm.pos). One thread.
-__device__ __noinline__ void next_segment(const Params& p, Smem& sm, int at) {
+// sm.seg[at ^ 1] (whose b, or the one after it, is the sequence at sm.pos). One
+// thread. n_most: the sequence's visible entries where they are known, else -1.
+__device__ __noinline__ void next_segment(const Params& p, Smem& sm, int at, int n_most) {
   const Segment& prev = sm.seg[at ^ 1];
   Segment s;
   s.g0 = prev.g0 + (uint32_t)prev.nt;
@@ -345,9 +367,9 @@ __device__ __noinline__ void next_segment(const Params& p, Smem& sm, int at) {
       ++s.b;
     }
     const int pieces = (int)min((long long)gridDim.x, sm.total), piece = (int)blockIdx.x;
-    s.n_most = visible_most(p, s.b, false);
+    s.n_most = n_most >= 0 ? n_most : visible_most(p, s.b, false);
     s.tiles = tiles_of(s.n_most);
-    s.blk = (int)((pos - sm.base) / s.tiles);
+    s.blk = (int)quotient(pos - sm.base, s.tiles);
     const long long pair = sm.base + (long long)s.blk * s.tiles;
     s.t0 = (int)(pos - pair);
     s.nt = (int)min((long long)(s.tiles - s.t0), sm.end - pos);
@@ -392,8 +414,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
     const int each = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, (int)threadIdx.x * each), b1 = min(p.B, b0 + each);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b)
-      mine += (long long)p.nblk * tiles_of(visible_most(p, b, blockIdx.x == 0));
+    int n_last = 0;
+    for (int b = b0; b < b1; ++b) {
+      n_last = visible_most(p, b, blockIdx.x == 0);
+      mine += (long long)p.nblk * tiles_of(n_last);
+    }
     sums[threadIdx.x] = mine;
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -430,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       sm.seg[1].g0 = sm.seg[1].used0 = sm.seg[1].used1 = 0;
       sm.pos = begin;
       sm.end = (int)blockIdx.x < pieces ? piece_begin((int)blockIdx.x + 1, pieces, total) : begin;
-      next_segment(p, sm, 0);
+      next_segment(p, sm, 0, each == 1 ? n_last : -1);
     }
   }
   tc_fence_before();
@@ -446,11 +471,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
     const uint32_t sph = sg & 1;                           // phase of the per-segment barriers
     const int nt = S.nt;
     if (threadIdx.x == 0) {
+      // the query block, for now in the second tile
       const int r0 = S.blk * kRows;
       const uint32_t qbytes = (uint32_t)min(kRows, p.Tq * p.Hq - r0) * kD * 2;
       mbar_arrive_expect_tx(&sm.bar.q_ld, qbytes);
-      bulk_load(vs + kVTile, p.q + ((size_t)S.b * p.Tq * p.Hq + r0) * kD, qbytes,
-                &sm.bar.q_ld);                             // the second tile, for now
+      bulk_load(vs + kVTile, p.q + ((size_t)S.b * p.Tq * p.Hq + r0) * kD, qbytes, &sm.bar.q_ld);
     }
 
     if (warp < kProducerWarps) {
@@ -460,27 +485,31 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       // Eight neighbouring lanes have four rows and two neighbouring j: rows lie
       // 288 bytes apart in the copy (32 more than a multiple of 128) and at other
       // swizzle phases in the tile, so their 16-byte accesses meet no bank twice.
-      const int u = lane & 15, half = lane >> 4;      // (staging the query block)
-      // the query block: see sparse attention's staging; rows are converted in
-      // place to fp16, scaled by a power of two per row (exact), then moved to
-      // tensor memory, thread (row, channel half) of two warps per quadrant
-      const int nr = min(kRows, p.Tq * p.Hq - S.blk * kRows);
+      // The query block goes to tensor memory as fp16, scaled per row by a power of
+      // two (which loses no bit of a bf16 value within 2^-24 of the row's largest).
+      // Warps w and w + 4 convert quadrant w's 16 rows in place, 16-byte chunk c of
+      // row h stored at c ^ (h & 7), and then move them, a thread 128 channels of one.
       auto stage_q = [&]() {
         const uint32_t qsm = vs_s + (uint32_t)kVTile;
         const bool ok = wait_hot_warp(&sm.bar.q_ld, sph, abort_flag);
-        if (ok) {
+        const int nr = min(kRows, p.Tq * p.Hq - S.blk * kRows);
+        if (ok && warp < 8) {
 #pragma unroll 1
-          for (int i0 = 0; i0 < (warp < 8 ? 8 : 0); i0 += 2) {
-            uint4 a[2], c[2];
-            uint32_t amax[2];
+          for (int i0 = 0; i0 < 8; i0 += 4) {
+            uint4 a[4], c[4];
+            uint32_t amax[4];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            for (int r = 0; r < 4; ++r) {
               const int hh = quad * 16 + (warp >> 2) * 8 + i0 + r;
               a[r] = c[r] = make_uint4(0, 0, 0, 0);
               if (hh < nr) {
                 a[r] = lds128(qsm + hh * 1024 + 16 * lane);
                 c[r] = lds128(qsm + hh * 1024 + 512 + 16 * lane);
               }
+            }
+            // (magnitudes of bf16 values order like their bits)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
               const uint32_t m = __vmaxu2(
                   __vmaxu2(__vmaxu2(a[r].x & 0x7fff7fffu, a[r].y & 0x7fff7fffu),
                            __vmaxu2(a[r].z & 0x7fff7fffu, a[r].w & 0x7fff7fffu)),
@@ -488,15 +517,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
                            __vmaxu2(c[r].z & 0x7fff7fffu, c[r].w & 0x7fff7fffu)));
               amax[r] = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
             }
-            __syncwarp();
+            __syncwarp();                            // read before it is rewritten
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            for (int r = 0; r < 4; ++r) {
               const int hh = quad * 16 + (warp >> 2) * 8 + i0 + r;
               if (hh >= nr) continue;
+              // 2^ex2 takes the largest magnitude to [2^14, 2^15)
               int ex2 = 0;
               const uint32_t eb = (amax[r] >> 7) & 0xffu;
               if (amax[r] != 0u && eb != 0xffu) ex2 = min(100, max(-100, 15 - ((int)eb - 126)));
-              const float up = copysignf(__uint_as_float((uint32_t)(127 + ex2) << 23), p.softmax_scale);
+              const float up =
+                  copysignf(__uint_as_float((uint32_t)(127 + ex2) << 23), p.softmax_scale);
               const uint32_t w[8] = {a[r].x, a[r].y, a[r].z, a[r].w,
                                      c[r].x, c[r].y, c[r].z, c[r].w};
               uint32_t f[8];
@@ -512,24 +543,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
           }
         }
         bar_sync(kBarProducers, kProducers);
-        const int h = quad * 16 + u;
+        if (warp < 8) {
+          const int ch = lane >> 4, h = quad * 16 + (lane & 15);
 #pragma unroll 1
-        for (int i = 2 * (warp >> 2); i < min(4, 2 * (warp >> 2) + 2); ++i) {
-          uint32_t w[32];
+          for (int i = 2 * (warp >> 2); i < 2 * (warp >> 2) + 2; ++i) {
+            uint32_t w[32];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (ok && h < nr)
-              v = lds128(qsm + h * 1024 + (((32 * half + 8 * i + j) ^ (h & 7)) << 4));
-            w[4 * j] = v.x;
-            w[4 * j + 1] = v.y;
-            w[4 * j + 2] = v.z;
-            w[4 * j + 3] = v.w;
+            for (int j = 0; j < 8; ++j) {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (ok && h < nr)
+                v = lds128(qsm + h * 1024 + (((32 * ch + 8 * i + j) ^ (h & 7)) << 4));
+              w[4 * j] = v.x;
+              w[4 * j + 1] = v.y;
+              w[4 * j + 2] = v.z;
+              w[4 * j + 3] = v.w;
+            }
+            // threads 0-15: channels 64 i .. + 63; threads 16-31: 256 further
+            tmem_st16x2_32<128>(tmem + lanes + kTmemQ + 32u * i, w);
           }
-          // threads 0-15: channels 64 i .. + 63; threads 16-31: 256 further
-          tmem_st16x2_32<128>(tmem + lanes + kTmemQ + 32u * i, w);
+          tc_fence_before();
         }
-        tc_fence_before();
         bar_sync(kBarProducers, kProducers);     // the block is read: its tile can be filled
         bar_arrive(kBarQ, kNumQ);
         return ok;
@@ -660,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       }
       for (int t = max(0, nt - 2); t < nt; ++t)
         bar_sync(kBarV + 2 * (t & 1) + 1, kNumV1);
-      if (lane == 0) next_segment(p, sm, (int)(sph ^ 1));
+      if (lane == 0) next_segment(p, sm, (int)(sph ^ 1), -1);
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMA issuer
       // The whole warp runs this with warp-uniform values and one elected lane
@@ -739,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       const bool real = r0 + h < p.Tq * p.Hq;
       const float hs = real ? fabsf(p.softmax_scale) * kLog2e * sm.qdown[h] : 0.0f;
       // entries that this row sees from the segment's first on
-      const int n_row = (real && p.nvalid ? visible(p, S.b, (r0 + h) / p.Hq, false) : S.n_most) - S.t0 * kT;
+      const int n_row = (real && p.nvalid ? visible(p, S.b, (r0 + h) / p.Hq) : S.n_most) - S.t0 * kT;
       const uint32_t g0 = S.g0, used0 = S.used0, used1 = S.used1;
       float m_ref = -INFINITY, l = 0.0f;
       bool ok = true;
@@ -871,32 +904,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       const int r0 = S.blk * kRows, slot = S.slot;
       const int nr = min(kRows, p.Tq * p.Hq - r0);
       const size_t row0 = (size_t)S.b * p.Tq * p.Hq + r0;
-#pragma unroll 1
+#pragma unroll 2
       for (int h = warp; h < nr; h += kThreads / 32) {
         const float2 ml = sm.mlf[h];
         const uint32_t row = vs_s + (uint32_t)(h * 2048);
-        if (slot < 0) {
-          // (a row that saw nothing has sum 0 and zeros in O)
-          const float f = ml.y > 0.0f ? 1.0f / ml.y : 0.0f;
+        // over the row sum (a row that saw nothing has sum 0 and zeros in O): the
+        // output in bf16, or a partial, a mean of values and so below 2^12, in fp16
+        const float f = ml.y > 0.0f ? 1.0f / ml.y : 0.0f;
+        uint4* dst = reinterpret_cast<uint4*>(
+            slot < 0 ? reinterpret_cast<uint16_t*>(p.out) + (row0 + h) * kD
+                     : reinterpret_cast<uint16_t*>(p.ws_o) + ((size_t)slot * kRows + h) * kD);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int c = 64 * k + 2 * lane;
-            const uint4 a = lds128(row + ((c ^ (h & 7)) << 4));
-            const uint4 d = lds128(row + (((c + 1) ^ (h & 7)) << 4));
-            reinterpret_cast<uint4*>(p.out + (row0 + h) * kD)[32 * k + lane] =
-                make_uint4(pack_bf162(__uint_as_float(a.x) * f, __uint_as_float(a.y) * f),
-                           pack_bf162(__uint_as_float(a.z) * f, __uint_as_float(a.w) * f),
-                           pack_bf162(__uint_as_float(d.x) * f, __uint_as_float(d.y) * f),
-                           pack_bf162(__uint_as_float(d.z) * f, __uint_as_float(d.w) * f));
-          }
-          if (p.lse && lane == 0)
+        for (int k = 0; k < 2; ++k) {
+          const int c = 64 * k + 2 * lane;
+          const uint4 a = lds128(row + ((c ^ (h & 7)) << 4));
+          const uint4 d = lds128(row + (((c + 1) ^ (h & 7)) << 4));
+          const float v[8] = {__uint_as_float(a.x) * f, __uint_as_float(a.y) * f,
+                              __uint_as_float(a.z) * f, __uint_as_float(a.w) * f,
+                              __uint_as_float(d.x) * f, __uint_as_float(d.y) * f,
+                              __uint_as_float(d.z) * f, __uint_as_float(d.w) * f};
+          dst[32 * k + lane] =
+              slot < 0 ? make_uint4(pack_bf162(v[0], v[1]), pack_bf162(v[2], v[3]),
+                                    pack_bf162(v[4], v[5]), pack_bf162(v[6], v[7]))
+                       : make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]),
+                                    pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+        }
+        if (lane == 0) {
+          if (slot >= 0)
+            p.ws_ml[(size_t)slot * kRows + h] = ml;
+          else if (p.lse)
             p.lse[row0 + h] = ml.y > 0.0f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.ws_o + ((size_t)slot * kRows + h) * kD);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[32 * k + lane] = lds128(row + (((32 * k + lane) ^ (h & 7)) << 4));
-          if (lane == 0) p.ws_ml[(size_t)slot * kRows + h] = ml;
         }
       }
     }
@@ -912,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
   if (threadIdx.x == 0 && *abort_flag) record_error(p.err, CSA2_ERR_TIMEOUT);
 }
 
-// Joins the pieces of one query row: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
+// Joins the pieces of one query row: out = sum_i w_i o_i / sum_i w_i, w_i = 2^(m_i - M) l_i.
 // 128 threads hold the row's channels, four groups of them take every fourth piece
 // (one group took 14 us for rows of 37 pieces: a chain of loads).
 constexpr int kCombineGroups = 4;
@@ -940,13 +977,15 @@ __global__ void __launch_bounds__(128 * kCombineGroups) paged_combine_kernel(con
 #pragma unroll 4
     for (int i = first + grp; i <= last; i += kCombineGroups) {
       const float2 ml = p.ws_ml[slot_of(i)];
-      const float4 v = *reinterpret_cast<const float4*>(p.ws_o + slot_of(i) * kD + 4 * d4);
-      const float w = exp2f(ml.x - M);                 // 0 for a piece that saw nothing
-      L = fmaf(w, ml.y, L);
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
+      const uint2 u = *reinterpret_cast<const uint2*>(p.ws_o + slot_of(i) * kD + 4 * d4);
+      const float w = exp2f(ml.x - M) * ml.y;          // 0 for a piece that saw nothing
+      const float2 v0 = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+      const float2 v1 = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+      L += w;
+      acc.x = fmaf(w, v0.x, acc.x);
+      acc.y = fmaf(w, v0.y, acc.y);
+      acc.z = fmaf(w, v1.x, acc.z);
+      acc.w = fmaf(w, v1.y, acc.w);
     }
   }
   part[grp][d4] = acc;
@@ -976,6 +1015,22 @@ int sm_count_of_device() {
   return n;
 }
 
+// The kernel's shared memory, allowed once per device.
+cudaError_t allow_shared_memory() {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(paged_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)kSmemBytes);
+  done[dev] = e == cudaSuccess;
+  return e;
+}
+
 // Pieces of the line of tiles: one per SM, never more than there can be tiles.
 int most_pieces(const fp4_kv_pages& pg, int B, int nblk) {
   const long long tiles = ((long long)pg.M * pg.page + kT - 1) / kT;
@@ -992,7 +1047,7 @@ size_t paged_attn_dense_workspace_bytes(const fp4_kv_pages& pg, int B, int Tq, i
   const int nblk = ceil_div(Tq * Hq, kRows);
   const size_t slots = 2 * (size_t)most_pieces(pg, B, nblk);
   return up256((size_t)B * nblk * sizeof(int4)) + up256(slots * kRows * sizeof(float2)) +
-         slots * kRows * kD * sizeof(float);
+         slots * kRows * kD * sizeof(__half);
 }
 
 cudaError_t launch_paged_attn_dense(const uint16_t* q, const fp4_kv_pages& pg, const int32_t* seq,
@@ -1019,11 +1074,9 @@ cudaError_t launch_paged_attn_dense(const uint16_t* q, const fp4_kv_pages& pg, c
   w += up256((size_t)B * p.nblk * sizeof(int4));
   p.ws_ml = reinterpret_cast<float2*>(w);
   w += up256(2 * (size_t)pieces * kRows * sizeof(float2));
-  p.ws_o = reinterpret_cast<float*>(w);
+  p.ws_o = reinterpret_cast<__half*>(w);
   p.err = err;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_tc_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)kSmemBytes);
+  cudaError_t e = allow_shared_memory();
   if (e != cudaSuccess) return e;
   e = launch_pdl(paged_attn_tc_kernel, dim3(pieces), dim3(kThreads), kSmemBytes, stream, dim3(1),
                  p);
