@@ -14,7 +14,10 @@
 //
 // Work is dealt out by tiles: the tiles of all (sequence, row block) pairs stand in
 // one line that is cut into as many equal pieces as there are SMs, so a ragged
-// batch keeps every SM busy. A pair that lies within one piece is written out;
+// batch keeps every SM busy. (Before each pair's tiles the line has kSetup units of
+// nothing, what a further pair costs a piece: its query block and its output take
+// as long as four tiles. Without them, pieces with two pairs ended 10 us after
+// the others, of 24 us.) A pair that lies within one piece is written out;
 // one that is cut leaves fp16 partials with their (maximum, sum), which
 // paged_combine_kernel joins. A sequence without entries has one empty tile.
 //
@@ -79,6 +82,7 @@ constexpr int kProducers = kProducerWarps * 32, kSoftmax = 4 * 32;
 constexpr int kNumQ = kProducers + 32 + kSoftmax, kNumP = kSoftmax + 32, kNumL = kProducers + 32;
 constexpr int kNumV0 = kProducers + 32, kNumV1 = kProducers + 64;
 constexpr int kNumS = kSoftmax + 32;
+constexpr int kSetup = 4;           // units of the line of tiles before each pair
 
 struct __align__(8) Bars {
   uint64_t q_ld, o_full, s_full[2], raw_full[2], v_free[2][2];   // v_free: [tile][half]
@@ -99,9 +103,9 @@ struct __align__(16) Smem {
   Segment seg[2];
   uint32_t tmem_slot;
   int abort_flag;
-  long long total;                  // tiles in all
-  long long pos, end;               // this piece's tiles not yet in a segment
-  long long base;                   // tiles before the sequence that pos lies in
+  long long total;                  // units of the line
+  long long pos, end;               // this piece's units not yet in a segment
+  long long base;                   // units before the sequence that pos lies in
   uint4 valid[4];                   // bit i of a tile's 128: entry i is there
   float2 mlf[kRows];                // (reference maximum, row sum)
   float qdown[kRows];               // the power of two each row was scaled up by, inverted
@@ -340,12 +344,14 @@ __device__ __forceinline__ int tiles_of(int n) { return max(1, (n + kT - 1) / kT
 __device__ __forceinline__ long long quotient(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
-// Piece i of `pieces` holds the tiles [piece_begin(i), piece_begin(i + 1)) of `total`.
+// Units of a sequence's (row block) pairs, and of one of them.
+__device__ __forceinline__ int pair_units(int n) { return kSetup + tiles_of(n); }
+// Piece i of `pieces` holds the units [piece_begin(i), piece_begin(i + 1)) of `total`.
 __device__ __forceinline__ long long piece_begin(int i, int pieces, long long total) {
   return quotient((long long)i * total, pieces);
 }
-__device__ __forceinline__ int piece_of(long long tile, int pieces, long long total) {
-  return (int)quotient((tile + 1) * pieces - 1, total);
+__device__ __forceinline__ int piece_of(long long unit, int pieces, long long total) {
+  return (int)quotient((unit + 1) * pieces - 1, total);
 }
 
 // Cuts the next segment off the piece: sm.seg[at] from its predecessor
@@ -360,25 +366,29 @@ __device__ __noinline__ void next_segment(const Params& p, Smem& sm, int at, int
   s.b = prev.b;
   s.nt = 0;
   s.blk = s.t0 = s.n_most = s.tiles = s.slot = 0;
-  const long long pos = sm.pos;
+  long long pos = sm.pos;
   if (pos < sm.end) {
-    if (prev.nt > 0 && pos == sm.base + (long long)p.nblk * prev.tiles) {
+    if (prev.nt > 0 && pos == sm.base + (long long)p.nblk * (kSetup + prev.tiles)) {
       sm.base = pos;
       ++s.b;
     }
     const int pieces = (int)min((long long)gridDim.x, sm.total), piece = (int)blockIdx.x;
     s.n_most = n_most >= 0 ? n_most : visible_most(p, s.b, false);
     s.tiles = tiles_of(s.n_most);
-    s.blk = (int)quotient(pos - sm.base, s.tiles);
-    const long long pair = sm.base + (long long)s.blk * s.tiles;
-    s.t0 = (int)(pos - pair);
-    s.nt = (int)min((long long)(s.tiles - s.t0), sm.end - pos);
-    const int slot = 2 * piece + (pos == piece_begin(piece, pieces, sm.total) ? 0 : 1);
-    s.slot = s.nt == s.tiles ? -1 : slot;
-    if (s.t0 == 0)
-      p.ws_info[(size_t)s.b * p.nblk + s.blk] =
-          make_int4(piece, piece_of(pair + s.tiles - 1, pieces, sm.total), slot, 0);
-    sm.pos = pos + s.nt;
+    const int units = kSetup + s.tiles;
+    s.blk = (int)quotient(pos - sm.base, units);
+    const long long first = sm.base + (long long)s.blk * units + kSetup;   // the pair's first tile
+    pos = max(pos, first);
+    s.t0 = (int)(pos - first);
+    s.nt = (int)max(0ll, min((long long)(s.tiles - s.t0), sm.end - pos));
+    if (s.nt > 0) {
+      const int slot = 2 * piece + (prev.nt > 0 ? 1 : 0);
+      s.slot = s.nt == s.tiles ? -1 : slot;
+      if (s.t0 == 0)
+        p.ws_info[(size_t)s.b * p.nblk + s.blk] =
+            make_int4(piece, piece_of(first + s.tiles - 1, pieces, sm.total), slot, 0);
+    }
+    sm.pos = s.nt > 0 ? pos + s.nt : sm.end;
   }
   sm.seg[at] = s;
 }
@@ -407,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
   if (warp == kMmaWarp) tmem_alloc(&sm.tmem_slot, kTmemCols);
   pdl_wait_and_release();
 
-  // ---- this CTA's piece: each thread adds up the tiles of a stretch of
-  // sequences; the one whose stretch holds the piece's first tile finds its sequence
+  // ---- this CTA's piece: each thread adds up the units of a stretch of
+  // sequences; the one whose stretch holds the piece's first unit finds its sequence
   {
     long long* sums = reinterpret_cast<long long*>(vs);
     const int each = (p.B + kThreads - 1) / kThreads;
@@ -417,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
     int n_last = 0;
     for (int b = b0; b < b1; ++b) {
       n_last = visible_most(p, b, blockIdx.x == 0);
-      mine += (long long)p.nblk * tiles_of(n_last);
+      mine += (long long)p.nblk * pair_units(n_last);
     }
     sums[threadIdx.x] = mine;
     __syncthreads();
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       long long at = before;
       int b = b0;
       for (; b + 1 < b1; ++b) {
-        const long long k = (long long)p.nblk * tiles_of(visible_most(p, b, false));
+        const long long k = (long long)p.nblk * pair_units(visible_most(p, b, false));
         if (begin < at + k) break;
         at += k;
       }
@@ -950,62 +960,50 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
 }
 
 // Joins the pieces of one query row: out = sum_i w_i o_i / sum_i w_i, w_i = 2^(m_i - M) l_i.
-// 128 threads hold the row's channels, four groups of them take every fourth piece
-// (one group took 14 us for rows of 37 pieces: a chain of loads).
-constexpr int kCombineGroups = 4;
+// Four rows per CTA, 64 threads each (8 channels a thread, one 16-byte load per
+// piece): rows come from few pieces when there are many of them, and a CTA of its
+// own for each, with its pieces shared out, took 10 us for 2280 rows.
+constexpr int kCombineRows = 4;
 
-__global__ void __launch_bounds__(128 * kCombineGroups) paged_combine_kernel(const Params p) {
-  __shared__ float4 part[kCombineGroups][128];
-  __shared__ float part_l[kCombineGroups];
+__global__ void __launch_bounds__(64 * kCombineRows) paged_combine_kernel(const Params p) {
   pdl_wait_and_release();
   const int per_seq = p.Tq * p.Hq;
-  const int r = blockIdx.x;                            // row of the sequence
+  const int r = blockIdx.x * kCombineRows + (threadIdx.x >> 6);    // row of the sequence
+  if (r >= per_seq) return;
   const size_t b = blockIdx.y;
   const int4 info = p.ws_info[b * p.nblk + r / kRows];
   const int first = info.x, last = info.y;
   if (first == last) return;
-  const int h = r % kRows, lane = threadIdx.x & 31;
-  const int grp = threadIdx.x >> 7, d4 = threadIdx.x & 127;
+  const int h = r % kRows, lane = threadIdx.x & 31, c = threadIdx.x & 63;
   auto slot_of = [&](int i) { return (size_t)(i == first ? info.z : 2 * i) * kRows + h; };
   float M = -INFINITY;
   for (int i = first + lane; i <= last; i += 32) M = fmaxf(M, p.ws_ml[slot_of(i)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float L = 0.0f;
-  float4 acc = make_float4(0, 0, 0, 0);
+  float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   if (M != -INFINITY) {
-#pragma unroll 4
-    for (int i = first + grp; i <= last; i += kCombineGroups) {
+#pragma unroll 8
+    for (int i = first; i <= last; ++i) {
       const float2 ml = p.ws_ml[slot_of(i)];
-      const uint2 u = *reinterpret_cast<const uint2*>(p.ws_o + slot_of(i) * kD + 4 * d4);
+      const uint4 u = *reinterpret_cast<const uint4*>(p.ws_o + slot_of(i) * kD + 8 * c);
       const float w = exp2f(ml.x - M) * ml.y;          // 0 for a piece that saw nothing
-      const float2 v0 = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-      const float2 v1 = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+      const uint32_t v[4] = {u.x, u.y, u.z, u.w};
       L += w;
-      acc.x = fmaf(w, v0.x, acc.x);
-      acc.y = fmaf(w, v0.y, acc.y);
-      acc.z = fmaf(w, v1.x, acc.z);
-      acc.w = fmaf(w, v1.y, acc.w);
-    }
-  }
-  part[grp][d4] = acc;
-  if (d4 == 0) part_l[grp] = L;
-  __syncthreads();
-  if (grp > 0) return;
 #pragma unroll
-  for (int k = 1; k < kCombineGroups; ++k) {
-    const float4 v = part[k][d4];
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
-    L += part_l[k];
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[k]));
+        acc[2 * k] = fmaf(w, f.x, acc[2 * k]);
+        acc[2 * k + 1] = fmaf(w, f.y, acc[2 * k + 1]);
+      }
+    }
   }
   const float inv = L > 0.0f ? 1.0f / L : 0.0f;
   const size_t row = b * per_seq + r;
-  *reinterpret_cast<uint2*>(p.out + row * kD + 4 * d4) =
-      make_uint2(pack_bf162(acc.x * inv, acc.y * inv), pack_bf162(acc.z * inv, acc.w * inv));
-  if (p.lse && threadIdx.x == 0) p.lse[row] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  reinterpret_cast<uint4*>(p.out + row * kD)[c] =
+      make_uint4(pack_bf162(acc[0] * inv, acc[1] * inv), pack_bf162(acc[2] * inv, acc[3] * inv),
+                 pack_bf162(acc[4] * inv, acc[5] * inv), pack_bf162(acc[6] * inv, acc[7] * inv));
+  if (p.lse && c == 0) p.lse[row] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
 int sm_count_of_device() {
@@ -1031,10 +1029,10 @@ cudaError_t allow_shared_memory() {
   return e;
 }
 
-// Pieces of the line of tiles: one per SM, never more than there can be tiles.
+// Pieces of the line of tiles: one per SM, never more than there can be units.
 int most_pieces(const fp4_kv_pages& pg, int B, int nblk) {
-  const long long tiles = ((long long)pg.M * pg.page + kT - 1) / kT;
-  const long long all = tiles * B * nblk;
+  const long long units = kSetup + ((long long)pg.M * pg.page + kT - 1) / kT;
+  const long long all = units * B * nblk;
   const int sms = sm_count_of_device();
   return (int)(all < sms ? all : sms);
 }
@@ -1081,8 +1079,8 @@ cudaError_t launch_paged_attn_dense(const uint16_t* q, const fp4_kv_pages& pg, c
   e = launch_pdl(paged_attn_tc_kernel, dim3(pieces), dim3(kThreads), kSmemBytes, stream, dim3(1),
                  p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_combine_kernel, dim3(Tq * Hq, B),
-                    dim3(128 * kCombineGroups), 0, stream, dim3(1), p);
+  return launch_pdl(paged_combine_kernel, dim3(ceil_div(Tq * Hq, kCombineRows), B),
+                    dim3(64 * kCombineRows), 0, stream, dim3(1), p);
 }
 
 }  // namespace csa2
