@@ -960,15 +960,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
 }
 
 // Joins the pieces of one query row: out = sum_i w_i o_i / sum_i w_i, w_i = 2^(m_i - M) l_i.
-// Four rows per CTA, 64 threads each (8 channels a thread, one 16-byte load per
-// piece): rows come from few pieces when there are many of them, and a CTA of its
-// own for each, with its pieces shared out, took 10 us for 2280 rows.
-constexpr int kCombineRows = 4;
-
-__global__ void __launch_bounds__(64 * kCombineRows) paged_combine_kernel(const Params p) {
+// 64 threads hold a row's 512 channels (one 16-byte load per piece). kGroups = 1:
+// four rows per CTA; 4: one row, its pieces shared out over four groups. Rows are
+// many when each comes from few pieces (2280 rows of 4 to 9: four rows per CTA 5 us
+// less than one), and few when they come from many (256 rows of 37: one per CTA).
+template <int kGroups>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const Params p) {
+  constexpr int kRowsPerCta = 4 / kGroups;
+  __shared__ float part[kGroups][64][9];               // (kGroups > 1) 8 channels, weight
   pdl_wait_and_release();
   const int per_seq = p.Tq * p.Hq;
-  const int r = blockIdx.x * kCombineRows + (threadIdx.x >> 6);    // row of the sequence
+  const int unit = threadIdx.x >> 6, grp = unit % kGroups;
+  const int r = blockIdx.x * kRowsPerCta + unit / kGroups;         // row of the sequence
   if (r >= per_seq) return;
   const size_t b = blockIdx.y;
   const int4 info = p.ws_info[b * p.nblk + r / kRows];
@@ -983,8 +986,8 @@ __global__ void __launch_bounds__(64 * kCombineRows) paged_combine_kernel(const 
   float L = 0.0f;
   float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   if (M != -INFINITY) {
-#pragma unroll 8
-    for (int i = first; i <= last; ++i) {
+#pragma unroll 4
+    for (int i = first + grp; i <= last; i += kGroups) {
       const float2 ml = p.ws_ml[slot_of(i)];
       const uint4 u = *reinterpret_cast<const uint4*>(p.ws_o + slot_of(i) * kD + 8 * c);
       const float w = exp2f(ml.x - M) * ml.y;          // 0 for a piece that saw nothing
@@ -996,6 +999,19 @@ __global__ void __launch_bounds__(64 * kCombineRows) paged_combine_kernel(const 
         acc[2 * k] = fmaf(w, f.x, acc[2 * k]);
         acc[2 * k + 1] = fmaf(w, f.y, acc[2 * k + 1]);
       }
+    }
+  }
+  if (kGroups > 1) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) part[grp][c][k] = acc[k];
+    part[grp][c][8] = L;
+    __syncthreads();                                   // (one row: the CTA is here or has left)
+    if (grp > 0) return;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] += part[g][c][k];
+      L += part[g][c][8];
     }
   }
   const float inv = L > 0.0f ? 1.0f / L : 0.0f;
@@ -1079,8 +1095,10 @@ cudaError_t launch_paged_attn_dense(const uint16_t* q, const fp4_kv_pages& pg, c
   e = launch_pdl(paged_attn_tc_kernel, dim3(pieces), dim3(kThreads), kSmemBytes, stream, dim3(1),
                  p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_combine_kernel, dim3(ceil_div(Tq * Hq, kCombineRows), B),
-                    dim3(64 * kCombineRows), 0, stream, dim3(1), p);
+  if ((long long)B * Tq * Hq <= 8 * sm_count_of_device())
+    return launch_pdl(paged_combine_kernel<4>, dim3(Tq * Hq, B), dim3(256), 0, stream, dim3(1), p);
+  return launch_pdl(paged_combine_kernel<1>, dim3(ceil_div(Tq * Hq, 4), B), dim3(256), 0, stream,
+                    dim3(1), p);
 }
 
 }  // namespace csa2
