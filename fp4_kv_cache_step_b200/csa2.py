@@ -460,9 +460,16 @@ def layer_step_workspace_bytes(mode, args: LayerArgs, shared: Csa2Shared) -> int
 
 
 # ------------------------------------------------------------------- paged cache
+def _at(t, name, device):
+    """A tensor's pointer, if it is on `device`."""
+    if t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    return t.data_ptr()
+
+
 def _i32(t, name, n, device):
     """A contiguous int32 CUDA tensor of n values on `device`: its pointer."""
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError("%s must be torch.int32, got %s" % (name, t.dtype))
     if t.numel() != n or not t.is_contiguous():
         raise ValueError("%s must be contiguous with %d values, got shape %s"
@@ -470,30 +477,27 @@ def _i32(t, name, n, device):
     return _at(t, name, device)
 
 
-def _at(t, name, device):
-    if t.device != device:
-        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
-    return t.data_ptr()
-
-
 def _call(name, device, *args):
     """The C call of that name on the current stream of `device`, with that
     device current (a default stream belongs to the current device)."""
-    fn = getattr(load(), name)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    fn = getattr(_lib or load(), name)
+    index = device.index
+    # (the raw handle: a Stream object costs more than the small calls' launch)
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != 0:
         _check(rc, name)
 
 
 def _scratch(workspace, need, device):
-    """(pointer, bytes) of the caller's workspace, or of a new one."""
+    """(tensor, pointer, bytes) of the caller's workspace, or of a new one."""
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
+        return workspace, workspace.data_ptr(), need
+    if workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % device)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 

@@ -10,13 +10,16 @@
 // One warp per head of a token (fp32, bf16 out) or per entry (fp64, so that a
 // value next to a border of the E2M1 grid falls to its own side: a borderline
 // flip would make the stored codes depend on the order of a sum). A lane holds
-// chunks of 8 channels (lane + 32 j), read as 16-byte words; the rotary part goes
-// through a per-warp strip of shared memory, so that either pair layout and any
-// first channel work alike; the cosines and sines of a token are computed once
-// per CTA and shared by its warps' heads. An entry's group of 16 channels is two
-// neighbouring lanes: one exchange gives its maximum, the codes of a lane are one
-// 32-bit word. Bound: HBM (a few dozen instructions per 16 bytes read and
-// written); at single tokens, the launch.
+// chunks of 8 channels (lane + 32 j), read as 16-byte words, two heads at a time;
+// the weights stay in its registers and the cosines and sines of a token are
+// computed once per CTA, while the first heads are on their way. Rotation:
+//   neighbouring channels are in one lane's chunk;
+//   halves R/2 apart are R/16 chunks apart: one exchange between lanes, where
+//   the rotary part lies within one round of 32 chunks on chunk borders;
+//   anything else goes through a per-warp strip of shared memory.
+// An entry's group of 16 channels is two neighbouring lanes: one exchange gives its
+// maximum, the codes of a lane are one 32-bit word. Bound: HBM (a few dozen
+// instructions per 16 bytes read and written); at single tokens, the launch.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -25,12 +28,14 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxD = 1024;
+
+enum : int { kNone = 0, kInLane = 1, kExchange = 2, kStrip = 3 };   // how channels rotate
 
 struct NormRope {
   csa2_norm_rope_args a;
   fp4_kv_pages pg;
   int shift;
+  int entry_blocks, entries_per_cta;
   int q_blocks;      // CTAs per token's heads
   int heads_per_cta;
   int* err;
@@ -74,7 +79,7 @@ __device__ __forceinline__ void pair_of(const csa2_norm_rope_args& a, int i, int
   *v = a.interleaved ? 2 * i + 1 : i + a.R / 2;
 }
 
-template <int J, typename F>
+template <typename F>
 __device__ __forceinline__ F warp_sum(F x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -157,7 +162,7 @@ __device__ void entry_row(const NormRope& p, int e, double* strip, const double*
     }
   }
   if (a.kv_norm) {
-    const double r = 1.0 / sqrt(warp_sum<J>(sum) / D + (double)a.eps);
+    const double r = 1.0 / sqrt(warp_sum(sum) / D + (double)a.eps);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int c0 = (lane + 32 * j) * 8;
@@ -215,87 +220,153 @@ __device__ void entry_row(const NormRope& p, int e, double* strip, const double*
   if (bad) record_error(p.err, CSA2_ERR_NONFINITE);
 }
 
-template <int J>
-__device__ void query_head(const NormRope& p, int t, int h, float* strip, const float* cs) {
-  const csa2_norm_rope_args& a = p.a;
+// Rotates the fp32 channels of a row held as chunks (see the top of the file).
+template <int J, int kPath>
+__device__ __forceinline__ void rotate_row(const csa2_norm_rope_args& a, float (&y)[J][8],
+                                           float* strip, const float* cs) {
   const int lane = threadIdx.x & 31;
-  const int D = a.D;
-  float y[J][8];
-  float sum = 0.0f;
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int c0 = (lane + 32 * j) * 8;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) y[j][k] = 0.0f;
-    if (c0 < D) load8(a.q, a.q_f32 != 0, (size_t)t * a.q_stride + (size_t)h * D + c0, y[j]);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) sum = fmaf(y[j][k], y[j][k], sum);
-  }
-  if (a.q_norm) {
-    const float r = 1.0f / sqrtf(warp_sum<J>(sum) / D + a.eps);
+  const int b = a.rot_begin, R = a.R;
+  if (kPath == kInLane) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int c0 = (lane + 32 * j) * 8;
-      if (c0 >= D) continue;
+      const int c0 = (lane + 32 * j) * 8 - b;          // in the rotary part; even
 #pragma unroll
-      for (int k = 0; k < 8; ++k) y[j][k] *= a.q_weight ? r * __ldg(a.q_weight + c0 + k) : r;
+      for (int k = 0; k < 8; k += 2) {
+        if (c0 + k >= 0 && c0 + k < R) {
+          const float2 t = *reinterpret_cast<const float2*>(cs + c0 + k);
+          const float u = y[j][k], v = y[j][k + 1];
+          y[j][k] = u * t.x - v * t.y;
+          y[j][k + 1] = v * t.x + u * t.y;
+        }
+      }
     }
-  }
-  if (a.R) rotate<J>(a, y, strip, cs);
+  } else if (kPath == kExchange) {
+    const int jr = b >> 8, first = (b >> 3) & 31, half = R >> 4;   // in chunks
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int c0 = (lane + 32 * j) * 8;
-    if (c0 < D)
-      __stcs(reinterpret_cast<uint4*>(a.q_out + ((size_t)t * a.Hq + h) * D + c0),
-             pack_bf16x8(y[j]));
+    for (int j = 0; j < J; ++j) {
+      if (j != jr) continue;                                       // the same for every lane
+      const int i = lane - first;
+      const bool mine = i >= 0 && i < 2 * half, low = i < half;
+      const int other = mine ? (low ? lane + half : lane - half) : lane;
+      const float* t = cs + (low ? i : i - half) * 16;             // pairs 8 i .. of (cos, sin)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float o = __shfl_sync(0xffffffffu, y[j][k], other);
+        if (mine) {
+          const float2 f = *reinterpret_cast<const float2*>(t + 2 * k);
+          y[j][k] = low ? y[j][k] * f.x - o * f.y : y[j][k] * f.x + o * f.y;
+        }
+      }
+    }
+  } else if (kPath == kStrip) {
+    rotate<J>(a, y, strip, cs);
   }
 }
 
-// CTAs [0, E) take an entry each (one warp works; they come first, being the
-// longest chains), the others heads_per_cta heads of a token.
-template <int J>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRope p) {
-  // cosines and sines of the R/2 pairs, then a strip of R channels per warp; an
-  // entry uses the same bytes as doubles (one warp)
+// CTAs [0, entry_blocks) take entries, one per warp (they come first, being the
+// longest chains); the others heads_per_cta heads of a token.
+template <int J, int kPath>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRope p) {
+  // queries: cosines and sines of the R/2 pairs, then a strip of R floats per warp;
+  // entries: per warp both as doubles
   extern __shared__ double smem[];
   pdl_wait_and_release();
   const csa2_norm_rope_args& a = p.a;
-  const int warp = threadIdx.x >> 5;
-  if ((int)blockIdx.x < a.E) {
-    const int e = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((int)blockIdx.x < p.entry_blocks) {
+    const int e = blockIdx.x * p.entries_per_cta + warp;
+    if (warp >= p.entries_per_cta || e >= a.E) return;
+    double* cs = smem + (size_t)warp * 2 * a.R;
     const int pos = __ldg(a.kv_pos + e);
-    if (threadIdx.x == 0 && pos < 0) record_error(p.err, CSA2_ERR_DEVICE_INDEX);
-    for (int i = threadIdx.x; i < a.R / 2; i += kThreads) {
+    if (lane == 0 && pos < 0) record_error(p.err, CSA2_ERR_DEVICE_INDEX);
+    for (int i = lane; i < a.R / 2; i += 32) {
       double s, c;
       // 2 pi frac: sincospi of twice the fraction
       sincospi((double)turn_fraction(pos, a.turns[i]) * 0x1p-63, &s, &c);
-      smem[2 * i] = c * (double)a.rot_scale;
-      smem[2 * i + 1] = (a.inverse ? -s : s) * (double)a.rot_scale;
+      cs[2 * i] = c * (double)a.rot_scale;
+      cs[2 * i + 1] = (a.inverse ? -s : s) * (double)a.rot_scale;
     }
-    __syncthreads();
-    if (warp == 0) entry_row<J>(p, e, smem + a.R, smem);
+    __syncwarp();
+    entry_row<J>(p, e, cs + a.R, cs);
     return;
   }
-  const int blk = blockIdx.x - a.E;
+  const int blk = blockIdx.x - p.entry_blocks;
   const int t = blk / p.q_blocks, h0 = (blk % p.q_blocks) * p.heads_per_cta;
-  const int pos = __ldg(a.pos + t);
-  if (threadIdx.x == 0 && pos < 0) record_error(p.err, CSA2_ERR_DEVICE_INDEX);
-  float* cs = reinterpret_cast<float*>(smem);
-  for (int i = threadIdx.x; i < a.R / 2; i += kThreads) {
-    float s, c;
-    sincospif((float)turn_fraction(pos, a.turns[i]) * 0x1p-63f, &s, &c);
-    cs[2 * i] = c * a.rot_scale;
-    cs[2 * i + 1] = (a.inverse ? -s : s) * a.rot_scale;
-  }
-  __syncthreads();
-  float* strip = cs + a.R + warp * a.R;
   const int h1 = min(a.Hq, h0 + p.heads_per_cta);
-  for (int h = h0 + warp; h < h1; h += kWarps) query_head<J>(p, t, h, strip, cs);
+  float* cs = reinterpret_cast<float*>(smem);
+  float* strip = cs + a.R + warp * a.R;
+  const int D = a.D;
+  constexpr int kRows = 2;                             // heads of a warp in flight
+  float y[kRows][J][8];
+  auto load = [&](int h, float (&v)[J][8]) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int c0 = (lane + 32 * j) * 8;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[j][k] = 0.0f;
+      if (c0 < D && h < h1)
+        load8(a.q, a.q_f32 != 0, (size_t)t * a.q_stride + (size_t)h * D + c0, v[j]);
+    }
+  };
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) load(h0 + warp + r * kWarps, y[r]);
+  float w[J][8];
+  const bool weighted = a.q_norm && a.q_weight != nullptr;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int c0 = (lane + 32 * j) * 8;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[j][k] = weighted && c0 < D ? __ldg(a.q_weight + c0 + k) : 1.0f;
+  }
+  if (kPath != kNone) {
+    const int pos = __ldg(a.pos + t);
+    if (threadIdx.x == 0 && pos < 0) record_error(p.err, CSA2_ERR_DEVICE_INDEX);
+    for (int i = threadIdx.x; i < a.R / 2; i += kThreads) {
+      float s, c;
+      sincospif((float)turn_fraction(pos, a.turns[i]) * 0x1p-63f, &s, &c);
+      cs[2 * i] = c * a.rot_scale;
+      cs[2 * i + 1] = (a.inverse ? -s : s) * a.rot_scale;
+    }
+    __syncthreads();
+  }
+  for (int h = h0 + warp; h < h1; h += kRows * kWarps) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int hr = h + r * kWarps;
+      if (hr >= h1) break;                             // the same for every lane
+      if (a.q_norm) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum = fmaf(y[r][j][k], y[r][j][k], sum);
+        const float f = 1.0f / sqrtf(warp_sum(sum) / D + a.eps);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y[r][j][k] *= f * w[j][k];
+      }
+      rotate_row<J, kPath>(a, y[r], strip, cs);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int c0 = (lane + 32 * j) * 8;
+        if (c0 < D)
+          __stcs(reinterpret_cast<uint4*>(a.q_out + ((size_t)t * a.Hq + hr) * D + c0),
+                 pack_bf16x8(y[r][j]));
+      }
+      load(hr + kRows * kWarps, y[r]);
+    }
+  }
 }
 
 template <int J>
-cudaError_t launch_j(const NormRope& p, unsigned grid, size_t smem, cudaStream_t stream) {
-  return launch_pdl(norm_rope_kernel<J>, dim3(grid), dim3(kThreads), smem, stream, dim3(1), p);
+cudaError_t launch_j(int path, const NormRope& p, unsigned grid, size_t smem,
+                     cudaStream_t stream) {
+  void (*kernel)(const NormRope) = path == kNone     ? norm_rope_kernel<J, kNone>
+                                   : path == kInLane ? norm_rope_kernel<J, kInLane>
+                                   : path == kExchange ? norm_rope_kernel<J, kExchange>
+                                                       : norm_rope_kernel<J, kStrip>;
+  return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, dim3(1), p);
 }
 
 }  // namespace
@@ -311,23 +382,36 @@ cudaError_t launch_qk_norm_rope(const csa2_norm_rope_args& a, const fp4_kv_pages
   int sms = 148, dev = 0;
   if (cudaGetDevice(&dev) == cudaSuccess)
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  // heads of a token per CTA: few tokens spread over the SMs a warp per head;
-  // many tokens share the cosines of a token among all of its heads
+  // heads of a token per CTA: few tokens spread over the SMs a warp per head; many
+  // tokens share the cosines of a token among up to 64 of its heads
   p.heads_per_cta = kWarps;
-  if ((long long)a.T * ceil_div(a.Hq > 0 ? a.Hq : 1, 4 * kWarps) >= 4ll * sms)
-    p.heads_per_cta = 4 * kWarps;
+  while (p.heads_per_cta < 8 * kWarps && p.heads_per_cta < a.Hq &&
+         (long long)a.T * ceil_div(a.Hq, 2 * p.heads_per_cta) >= 8ll * sms)
+    p.heads_per_cta *= 2;
   p.q_blocks = a.T > 0 ? ceil_div(a.Hq, p.heads_per_cta) : 0;
-  const long long grid = (long long)a.E + (long long)a.T * p.q_blocks;
+  // entries: as many warps as 48 KB of strips allow (R = 1024: three)
+  const size_t per_entry = 2 * (size_t)a.R * sizeof(double);
+  p.entries_per_cta = per_entry * kWarps <= 48 * 1024 ? kWarps : (int)(48 * 1024 / per_entry);
+  // few entries: a CTA each, as their chains are what a small call waits for
+  if (a.E <= sms) p.entries_per_cta = 1;
+  p.entry_blocks = ceil_div(a.E, p.entries_per_cta);
+  const long long grid = (long long)p.entry_blocks + (long long)a.T * p.q_blocks;
   if (grid == 0) return cudaSuccess;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-  const size_t smem = 2 * (size_t)a.R * sizeof(double) > (1 + kWarps) * (size_t)a.R * sizeof(float)
-                          ? 2 * (size_t)a.R * sizeof(double)
-                          : (1 + kWarps) * (size_t)a.R * sizeof(float);
+  int path = kStrip;
+  if (a.R == 0) path = kNone;
+  else if (a.interleaved && a.rot_begin % 2 == 0) path = kInLane;
+  else if (!a.interleaved && a.R % 16 == 0 && a.rot_begin % 8 == 0 &&
+           a.rot_begin / 256 == (a.rot_begin + a.R - 1) / 256)
+    path = kExchange;
+  const size_t for_entries = a.E > 0 ? p.entries_per_cta * per_entry : 0;
+  const size_t for_queries = (path == kStrip ? 1 + kWarps : 1) * (size_t)a.R * sizeof(float);
+  const size_t smem = for_entries > for_queries ? for_entries : for_queries;
   switch (ceil_div(a.D, 256)) {
-    case 1: return launch_j<1>(p, (unsigned)grid, smem, stream);
-    case 2: return launch_j<2>(p, (unsigned)grid, smem, stream);
-    case 3: return launch_j<3>(p, (unsigned)grid, smem, stream);
-    default: return launch_j<4>(p, (unsigned)grid, smem, stream);
+    case 1: return launch_j<1>(path, p, (unsigned)grid, smem, stream);
+    case 2: return launch_j<2>(path, p, (unsigned)grid, smem, stream);
+    case 3: return launch_j<3>(path, p, (unsigned)grid, smem, stream);
+    default: return launch_j<4>(path, p, (unsigned)grid, smem, stream);
   }
 }
 
