@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -460,33 +461,39 @@ def layer_step_workspace_bytes(mode, args: LayerArgs, shared: Csa2Shared) -> int
 
 
 # ------------------------------------------------------------------- paged cache
-def _at(t, name, device):
-    """A tensor's pointer, if it is on `device`."""
-    if t.device != device:
-        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+# (The calls below take microseconds on the GPU, so their checks avoid what costs
+# as much on the host: device objects, Stream objects, keyword parsing.)
+_BF16, _F32, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.int32, torch.int64,
+                                torch.uint8)
+
+
+def _at(t, name, index):
+    """A tensor's pointer, if it is on CUDA device `index`."""
+    if t.get_device() != index:
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, index, t.device))
     return t.data_ptr()
 
 
-def _i32(t, name, n, device):
-    """A contiguous int32 CUDA tensor of n values on `device`: its pointer."""
-    if t.dtype is not torch.int32:
-        raise TypeError("%s must be torch.int32, got %s" % (name, t.dtype))
+def _vec(t, name, dtype, n, index):
+    """A contiguous tensor of n values on CUDA device `index`: its pointer."""
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.numel() != n or not t.is_contiguous():
         raise ValueError("%s must be contiguous with %d values, got shape %s"
                          % (name, n, tuple(t.shape)))
-    return _at(t, name, device)
+    if t.get_device() != index:
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, index, t.device))
+    return t.data_ptr()
 
 
-def _call(name, device, *args):
-    """The C call of that name on the current stream of `device`, with that
-    device current (a default stream belongs to the current device)."""
+def _call(name, index, *args):
+    """The C call of that name on the current stream of CUDA device `index`, with
+    that device current (a default stream belongs to the current device)."""
     fn = getattr(_lib or load(), name)
-    index = device.index
-    # (the raw handle: a Stream object costs more than the small calls' launch)
     if index == torch._C._cuda_getDevice():
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != 0:
         _check(rc, name)
@@ -495,7 +502,7 @@ def _call(name, device, *args):
 def _scratch(workspace, need, device):
     """(tensor, pointer, bytes) of the caller's workspace, or of a new one."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = torch.empty(need, dtype=_U8, device=device)
         return workspace, workspace.data_ptr(), need
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % device)
@@ -509,25 +516,25 @@ class Fp4Pages:
 
     def __init__(self, rows: torch.Tensor, table: torch.Tensor, length: torch.Tensor,
                  refs: torch.Tensor):
-        _want(rows, torch.uint8, "rows", 3)
-        _want(table, torch.int32, "table", 2)
-        _want(length, torch.int32, "length", 1)
-        _want(refs, torch.int32, "refs", 1)
+        _want(rows, _U8, "rows", 3)
+        _want(table, _I32, "table", 2)
+        _want(length, _I32, "length", 1)
+        _want(refs, _I32, "refs", 1)
         P, page, rb = rows.shape
         S, M = table.shape
-        if rb % 72 != 0:
+        if rb == 0 or rb % 72 != 0:
             raise ValueError("rows of %d bytes hold no multiple of 128 channels" % rb)
         if length.shape[0] != S or refs.shape[0] != P:
             raise ValueError("length and refs must have S=%d and P=%d values" % (S, P))
         if not rows.is_cuda:
             raise ValueError("expected CUDA tensors")
+        self.device, self.index = rows.device, rows.get_device()
         for t, name in ((rows, "rows"), (table, "table"), (length, "length"), (refs, "refs")):
-            _at(t, name, rows.device)
+            _at(t, name, self.index)
             if not t.is_contiguous():
                 raise ValueError("expected contiguous %s" % name)
         self.rows, self.table, self.length, self.refs = rows, table, length, refs
         self.P, self.page, self.D, self.S, self.M = P, page, rb // 72 * 128, S, M
-        self.device = rows.device
         self._c = PagesStruct(rows.data_ptr(), table.data_ptr(), length.data_ptr(),
                               refs.data_ptr(), P, page, self.D, S, M)
         self.ref = ctypes.byref(self._c)
@@ -535,10 +542,10 @@ class Fp4Pages:
     @classmethod
     def empty(cls, P: int, page: int, D: int, S: int, M: int, device="cuda") -> "Fp4Pages":
         """A cache of P free pages and S empty slots of up to M pages."""
-        return cls(torch.zeros((P, page, g16_row_bytes(D)), dtype=torch.uint8, device=device),
-                   torch.full((S, M), -1, dtype=torch.int32, device=device),
-                   torch.zeros(S, dtype=torch.int32, device=device),
-                   torch.zeros(P, dtype=torch.int32, device=device))
+        return cls(torch.zeros((P, page, g16_row_bytes(D)), dtype=_U8, device=device),
+                   torch.full((S, M), -1, dtype=_I32, device=device),
+                   torch.zeros(S, dtype=_I32, device=device),
+                   torch.zeros(P, dtype=_I32, device=device))
 
 
 def fp4_kv_pages_resize(pages: Fp4Pages, seq: torch.Tensor, new_len: torch.Tensor,
@@ -546,31 +553,31 @@ def fp4_kv_pages_resize(pages: Fp4Pages, seq: torch.Tensor, new_len: torch.Tenso
     """Slots seq int32 [n] get new_len int32 [n] entries: pages behind are given
     back, free ones taken lowest first; a shared, partly filled last page that
     grows is copied. Length 0 frees a slot."""
-    n = seq.numel()
-    a, b = _i32(seq, "seq", n, pages.device), _i32(new_len, "new_len", n, pages.device)
+    n, index = seq.numel(), pages.index
+    a, b = _vec(seq, "seq", _I32, n, index), _vec(new_len, "new_len", _I32, n, index)
     ws, p, size = _scratch(workspace, load().fp4_kv_pages_resize_workspace_bytes(pages.ref, n),
                            pages.device)
-    _call("fp4_kv_pages_resize", pages.device, pages.ref, a, b, n, p, size)
+    _call("fp4_kv_pages_resize", index, pages.ref, a, b, n, p, size)
 
 
 def fp4_kv_pages_fork(pages: Fp4Pages, src: torch.Tensor, dst: torch.Tensor,
                       workspace: Optional[torch.Tensor] = None) -> None:
     """Slot dst[i] becomes a copy of slot src[i] (int32 [n], at once): the pages
     are shared, what dst[i] held is given back."""
-    n = src.numel()
-    a, b = _i32(src, "src", n, pages.device), _i32(dst, "dst", n, pages.device)
+    n, index = src.numel(), pages.index
+    a, b = _vec(src, "src", _I32, n, index), _vec(dst, "dst", _I32, n, index)
     ws, p, size = _scratch(workspace, load().fp4_kv_pages_fork_workspace_bytes(pages.ref, n),
                            pages.device)
-    _call("fp4_kv_pages_fork", pages.device, pages.ref, a, b, n, p, size)
+    _call("fp4_kv_pages_fork", index, pages.ref, a, b, n, p, size)
 
 
 def fp4_kv_pages_compact(pages: Fp4Pages, used: Optional[torch.Tensor] = None,
                          workspace: Optional[torch.Tensor] = None) -> None:
     """Move the U pages in use to the places [0, U); used int32 [1] receives U."""
-    u = None if used is None else _i32(used, "used", 1, pages.device)
+    u = None if used is None else _vec(used, "used", _I32, 1, pages.index)
     ws, p, size = _scratch(workspace, load().fp4_kv_pages_compact_workspace_bytes(pages.ref),
                            pages.device)
-    _call("fp4_kv_pages_compact", pages.device, pages.ref, u, p, size)
+    _call("fp4_kv_pages_compact", pages.index, pages.ref, u, p, size)
 
 
 # ------------------------------------------------------------------- norm, rotation, append
@@ -584,14 +591,16 @@ def csa2_rope_turns(R: int, base: float = 10000.0, scaling: str = "plain", facto
     each pair, times 2^64 (computed on the host, then copied to `device`)."""
     if scaling not in _ROPE_SCALING:
         raise ValueError("scaling must be one of %s" % ", ".join(_ROPE_SCALING))
-    turns = torch.empty(max(0, R) // 2, dtype=torch.int64)
+    turns = torch.empty(max(0, R) // 2, dtype=_I64)
     _check(load().csa2_rope_turns(int(R), float(base), _ROPE_SCALING[scaling], float(factor),
                                   float(context), float(fast), float(slow),
                                   turns.data_ptr() if turns.numel() else None), "csa2_rope_turns")
     return turns.to(device)
 
 
-_ROW_TYPES = (torch.bfloat16, torch.float32)
+# csa2_norm_rope_args, packed in one go (checked against NormRopeArgs below)
+_ROPE_PACK = struct.Struct("@5i2fxxxxP4iPqPPPiiixxxxPqPPPPP")
+assert _ROPE_PACK.size == ctypes.sizeof(NormRopeArgs)
 
 
 def csa2_qk_norm_rope(turns: torch.Tensor, rot_begin: int, interleaved: bool = True,
@@ -610,73 +619,73 @@ def csa2_qk_norm_rope(turns: torch.Tensor, rot_begin: int, interleaved: bool = T
     [rot_begin, rot_begin + R) turn by pos (kv_pos) int32 times `turns` [R/2]."""
     if q is None and kv is None:
         raise ValueError("nothing to do: give q, kv or both")
-    device = (q if q is not None else kv).device
-    _want(turns, torch.int64, "turns", 1)
-    a = NormRopeArgs()
-    a.R, a.rot_begin = 2 * turns.shape[0], int(rot_begin)
-    a.interleaved, a.inverse = int(bool(interleaved)), int(bool(inverse))
-    a.rot_scale, a.eps = rot_scale, eps
-    if a.R:
-        if not turns.is_contiguous():
-            raise ValueError("expected contiguous turns")
-        a.turns = _at(turns, "turns", device)
+    index = (q if q is not None else kv).get_device()
+    R2 = turns.numel()
+    if turns.dim() != 1:
+        raise ValueError("turns must have 1 dim, got shape %s" % (tuple(turns.shape),))
+    p_turns = _vec(turns, "turns", _I64, R2, index) if R2 else 0
+    D = T = H = q_f32 = q_stride = p_q = p_pos = p_qw = p_qo = 0
+    E = kv_f32 = kv_stride = p_kv = p_kp = p_kw = p_seq = p_entry = p_ko = 0
     if q is not None:
-        if q.dtype not in _ROW_TYPES:
-            raise TypeError("q must be bfloat16 or float32, got %s" % q.dtype)
-        if q.dim() != 3 or (q.numel() and (q.stride(2) != 1 or (q.shape[1] > 1 and
-                                                               q.stride(1) != q.shape[2]))):
-            raise ValueError("q must be [T][Hq][D] with contiguous heads, got shape %s strides %s"
-                             % (tuple(q.shape), q.stride()))
+        if q.dim() != 3:
+            raise ValueError("q must be [T][Hq][D], got shape %s" % (tuple(q.shape),))
         T, H, D = q.shape
+        q_stride, head, one = q.stride()
+        q_f32 = q.dtype is _F32
+        if not q_f32 and q.dtype is not _BF16:
+            raise TypeError("q must be bfloat16 or float32, got %s" % q.dtype)
+        if T and (one != 1 or (H > 1 and head != D)):
+            raise ValueError("q must have contiguous heads, got shape %s strides %s"
+                             % (tuple(q.shape), q.stride()))
+        if T <= 1:
+            q_stride = H * D
         if q_out is None:
-            q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=device)
-        _want(q_out, torch.bfloat16, "q_out", 3)
-        if q_out.shape != q.shape or not q_out.is_contiguous():
-            raise ValueError("q_out must be contiguous and shaped as q")
+            q_out = torch.empty((T, H, D), dtype=_BF16, device=q.device)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must be shaped as q")
         if pos is None:
             raise ValueError("q needs pos")
-        a.T, a.Hq, a.D, a.q_norm, a.q_f32 = T, H, D, int(bool(q_norm)), q.dtype == torch.float32
-        a.q, a.q_out = _at(q, "q", device), _at(q_out, "q_out", device)
-        a.q_stride = q.stride(0) if T > 1 else H * D
-        a.pos = _i32(pos, "pos", T, device)
+        p_q, p_qo = _at(q, "q", index), _vec(q_out, "q_out", _BF16, T * H * D, index)
+        p_pos = _vec(pos, "pos", _I32, T, index)
         if q_weight is not None:
-            a.q_weight = _weight(q_weight, "q_weight", D, device)
+            p_qw = _vec(q_weight, "q_weight", _F32, D, index)
     if kv is not None:
-        if kv.dtype not in _ROW_TYPES:
+        if kv.dim() != 2:
+            raise ValueError("kv must be [E][D], got shape %s" % (tuple(kv.shape),))
+        E, channels = kv.shape
+        kv_stride, one = kv.stride()
+        kv_f32 = kv.dtype is _F32
+        if not kv_f32 and kv.dtype is not _BF16:
             raise TypeError("kv must be bfloat16 or float32, got %s" % kv.dtype)
-        if kv.dim() != 2 or (kv.numel() and kv.stride(1) != 1):
-            raise ValueError("kv must be [E][D] with contiguous rows, got shape %s strides %s"
-                             % (tuple(kv.shape), kv.stride()))
-        E, D = kv.shape
-        if q is not None and D != a.D:
-            raise ValueError("q and kv must have as many channels, got %d and %d" % (a.D, D))
+        if E and one != 1:
+            raise ValueError("kv must have contiguous rows, got strides %s" % (kv.stride(),))
+        if q is not None and channels != D:
+            raise ValueError("q and kv must have as many channels, got %d and %d" % (D, channels))
+        D = channels
+        if E <= 1:
+            kv_stride = D
         if pages is None or kv_pos is None or seq is None or entry is None:
             raise ValueError("kv needs kv_pos, pages, seq and entry")
-        if pages.device != device:
-            raise ValueError("pages must be on %s, got %s" % (device, pages.device))
-        a.E, a.D, a.kv_norm, a.kv_f32 = E, D, int(bool(kv_norm)), kv.dtype == torch.float32
-        a.kv = _at(kv, "kv", device)
-        a.kv_stride = kv.stride(0) if E > 1 else D
-        a.kv_pos = _i32(kv_pos, "kv_pos", E, device)
-        a.seq, a.entry = _i32(seq, "seq", E, device), _i32(entry, "entry", E, device)
+        if pages.index != index:
+            raise ValueError("pages must be on cuda:%d, got %s" % (index, pages.device))
+        p_kv = _at(kv, "kv", index)
+        p_kp = _vec(kv_pos, "kv_pos", _I32, E, index)
+        p_seq = _vec(seq, "seq", _I32, E, index)
+        p_entry = _vec(entry, "entry", _I32, E, index)
         if kv_weight is not None:
-            a.kv_weight = _weight(kv_weight, "kv_weight", D, device)
+            p_kw = _vec(kv_weight, "kv_weight", _F32, D, index)
         if kv_out is not None:
-            _want(kv_out, torch.bfloat16, "kv_out", 2)
-            if kv_out.shape != kv.shape or not kv_out.is_contiguous():
-                raise ValueError("kv_out must be contiguous and shaped as kv")
-            a.kv_out = _at(kv_out, "kv_out", device)
-    if device.type != "cuda":
+            if kv_out.shape != kv.shape:
+                raise ValueError("kv_out must be shaped as kv")
+            p_ko = _vec(kv_out, "kv_out", _BF16, E * D, index)
+    if index < 0:
         raise ValueError("expected CUDA tensors")
-    _call("csa2_qk_norm_rope", device, ctypes.byref(a), pages.ref if pages is not None else None)
+    args = NormRopeArgs.from_buffer_copy(_ROPE_PACK.pack(
+        D, 2 * R2, rot_begin, bool(interleaved), bool(inverse), rot_scale, eps, p_turns, T, H,
+        bool(q_norm), q_f32, p_q, q_stride, p_pos, p_qw, p_qo, E, bool(kv_norm), kv_f32, p_kv,
+        kv_stride, p_kp, p_kw, p_seq, p_entry, p_ko))
+    _call("csa2_qk_norm_rope", index, ctypes.byref(args), pages.ref if pages is not None else None)
     return q_out, kv_out
-
-
-def _weight(t, name, D, device):
-    _want(t, torch.float32, name, 1)
-    if t.shape[0] != D or not t.is_contiguous():
-        raise ValueError("%s must be contiguous with D=%d values" % (name, D))
-    return _at(t, name, device)
 
 
 def csa2_paged_attn(q: torch.Tensor, pages: Fp4Pages, softmax_scale: float,
@@ -687,34 +696,35 @@ def csa2_paged_attn(q: torch.Tensor, pages: Fp4Pages, softmax_scale: float,
     """q bf16 [B][Tq][Hq][512] over slots seq int32 [B] (None: slot b) of a paged
     cache: all of the first nvalid int32 [B][Tq] entries (None: the slot's length),
     or those listed in topk_idx int32 [B][Tq][K] -> (out bf16, lse float32 or None)."""
-    _want(q, torch.bfloat16, "q", 4)
-    device = pages.device
+    if q.dim() != 4:
+        raise ValueError("q must be [B][Tq][Hq][D], got shape %s" % (tuple(q.shape),))
     B, Tq, H, D = q.shape
+    index, device = pages.index, pages.device
     if D != pages.D:
         raise ValueError("q has %d channels, the pages %d" % (D, pages.D))
-    if not q.is_contiguous():
-        raise ValueError("expected a contiguous q")
-    K = 0
+    p_q = _vec(q, "q", _BF16, B * Tq * H * D, index)
+    p_seq = None if seq is None else _vec(seq, "seq", _I32, B, index)
+    p_nv = None if nvalid is None else _vec(nvalid, "nvalid", _I32, B * Tq, index)
+    K, p_ids = 0, None
     if topk_idx is not None:
-        _want(topk_idx, torch.int32, "topk_idx", 3)
+        if topk_idx.dim() != 3 or topk_idx.shape[2] == 0:
+            raise ValueError("topk_idx must be [B][Tq][K] with K >= 1, got shape %s"
+                             % (tuple(topk_idx.shape),))
         K = topk_idx.shape[2]
-        if K == 0:
-            raise ValueError("topk_idx must list at least one place")
+        p_ids = _vec(topk_idx, "topk_idx", _I32, B * Tq * K, index)
     if out is None:
         out = torch.empty_like(q)
-    elif out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("out must be bfloat16, contiguous and shaped as q")
-    if want_lse and lse is None:
-        lse = torch.empty((B, Tq, H), dtype=torch.float32, device=device)
-    elif want_lse and (lse.dtype != torch.float32 or lse.shape != q.shape[:3]
-                       or not lse.is_contiguous()):
-        raise ValueError("lse must be float32, contiguous and [B][Tq][Hq]")
+    elif out.shape != q.shape:
+        raise ValueError("out must be shaped as q")
+    p_lse = None
+    if want_lse:
+        if lse is None:
+            lse = torch.empty((B, Tq, H), dtype=_F32, device=device)
+        elif lse.shape != q.shape[:3]:
+            raise ValueError("lse must be [B][Tq][Hq]")
+        p_lse = _vec(lse, "lse", _F32, B * Tq * H, index)
     ws, p, size = _scratch(workspace,
                            load().csa2_paged_attn_workspace_bytes(pages.ref, B, Tq, H, K), device)
-    _call("csa2_paged_attn", device, _at(q, "q", device), pages.ref,
-          None if seq is None else _i32(seq, "seq", B, device),
-          None if nvalid is None else _i32(nvalid, "nvalid", B * Tq, device),
-          None if topk_idx is None else _i32(topk_idx, "topk_idx", B * Tq * K, device),
-          B, Tq, H, K, float(softmax_scale), _at(out, "out", device),
-          _at(lse, "lse", device) if want_lse else None, p, size)
+    _call("csa2_paged_attn", index, p_q, pages.ref, p_seq, p_nv, p_ids, B, Tq, H, K,
+          softmax_scale, _vec(out, "out", _BF16, B * Tq * H * D, index), p_lse, p, size)
     return out, (lse if want_lse else None)

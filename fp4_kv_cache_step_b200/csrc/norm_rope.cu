@@ -13,7 +13,7 @@
 // chunks of 8 channels (lane + 32 j), read as 16-byte words, two heads at a time;
 // the weights stay in its registers and the cosines and sines of a token are
 // computed once per CTA, while the first heads are on their way. Rotation:
-//   neighbouring channels are in one lane's chunk;
+//   neighbouring channels are in one lane's chunk, where the rotary part is whole chunks;
 //   halves R/2 apart are R/16 chunks apart: one exchange between lanes, where
 //   the rotary part lies within one round of 32 chunks on chunk borders;
 //   anything else goes through a per-warp strip of shared memory.
@@ -30,6 +30,28 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 
 enum : int { kNone = 0, kInLane = 1, kExchange = 2, kStrip = 3 };   // how channels rotate
+
+// Two floats in one 64-bit register: half the instructions of separate ones.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
 struct NormRope {
   csa2_norm_rope_args a;
@@ -220,24 +242,25 @@ __device__ void entry_row(const NormRope& p, int e, double* strip, const double*
   if (bad) record_error(p.err, CSA2_ERR_NONFINITE);
 }
 
-// Rotates the fp32 channels of a row held as chunks (see the top of the file).
+// Rotates the fp32 channels of a row held as chunks of four pairs (see the top of
+// the file).
 template <int J, int kPath>
-__device__ __forceinline__ void rotate_row(const csa2_norm_rope_args& a, float (&y)[J][8],
+__device__ __forceinline__ void rotate_row(const csa2_norm_rope_args& a, uint64_t (&y)[J][4],
                                            float* strip, const float* cs) {
   const int lane = threadIdx.x & 31;
   const int b = a.rot_begin, R = a.R;
   if (kPath == kInLane) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int c0 = (lane + 32 * j) * 8 - b;          // in the rotary part; even
+      const int c0 = (lane + 32 * j) * 8 - b;          // in the rotary part; whole chunks
+      if (c0 < 0 || c0 >= R) continue;
+      const float4 t0 = *reinterpret_cast<const float4*>(cs + c0);
+      const float4 t1 = *reinterpret_cast<const float4*>(cs + c0 + 4);
+      const float c[4] = {t0.x, t0.z, t1.x, t1.z}, s[4] = {t0.y, t0.w, t1.y, t1.w};
 #pragma unroll
-      for (int k = 0; k < 8; k += 2) {
-        if (c0 + k >= 0 && c0 + k < R) {
-          const float2 t = *reinterpret_cast<const float2*>(cs + c0 + k);
-          const float u = y[j][k], v = y[j][k + 1];
-          y[j][k] = u * t.x - v * t.y;
-          y[j][k + 1] = v * t.x + u * t.y;
-        }
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = unpack2(y[j][k]);
+        y[j][k] = pack2(v.x * c[k] - v.y * s[k], v.y * c[k] + v.x * s[k]);
       }
     }
   } else if (kPath == kExchange) {
@@ -250,23 +273,39 @@ __device__ __forceinline__ void rotate_row(const csa2_norm_rope_args& a, float (
       const int other = mine ? (low ? lane + half : lane - half) : lane;
       const float* t = cs + (low ? i : i - half) * 16;             // pairs 8 i .. of (cos, sin)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float o = __shfl_sync(0xffffffffu, y[j][k], other);
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t o2 = __shfl_sync(0xffffffffu, y[j][k], other);
         if (mine) {
-          const float2 f = *reinterpret_cast<const float2*>(t + 2 * k);
-          y[j][k] = low ? y[j][k] * f.x - o * f.y : y[j][k] * f.x + o * f.y;
+          const float2 v = unpack2(y[j][k]), o = unpack2(o2);
+          const float4 f = *reinterpret_cast<const float4*>(t + 4 * k);
+          const float s0 = low ? -f.y : f.y, s1 = low ? -f.w : f.w;
+          y[j][k] = pack2(v.x * f.x + o.x * s0, v.y * f.z + o.y * s1);
         }
       }
     }
   } else if (kPath == kStrip) {
-    rotate<J>(a, y, strip, cs);
+    float x[J][8];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = unpack2(y[j][k]);
+        x[j][2 * k] = v.x;
+        x[j][2 * k + 1] = v.y;
+      }
+    rotate<J>(a, x, strip, cs);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[j][k] = pack2(x[j][2 * k], x[j][2 * k + 1]);
   }
 }
 
 // CTAs [0, entry_blocks) take entries, one per warp (they come first, being the
 // longest chains); the others heads_per_cta heads of a token.
-template <int J, int kPath>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRope p) {
+// (64 registers a thread where they suffice: 32 warps per SM, 2 KB each in flight)
+template <int J, int kPath, bool kWide>
+__global__ void __launch_bounds__(kThreads, J <= 2 ? 4 : 2) norm_rope_kernel(const __grid_constant__ NormRope p) {
   // queries: cosines and sines of the R/2 pairs, then a strip of R floats per warp;
   // entries: per warp both as doubles
   extern __shared__ double smem[];
@@ -296,27 +335,35 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   float* cs = reinterpret_cast<float*>(smem);
   float* strip = cs + a.R + warp * a.R;
   const int D = a.D;
-  constexpr int kRows = 2;                             // heads of a warp in flight
-  float y[kRows][J][8];
-  auto load = [&](int h, float (&v)[J][8]) {
+  constexpr int kRows = kWide ? 1 : 2;                 // heads of a warp in flight
+  constexpr int kVecs = kWide ? 2 : 1;                 // 16-byte words of a chunk
+  uint4 raw[kRows][J][kVecs];
+  const float inv_d = 1.0f / D;
+  const int esz = kWide ? 4 : 2;
+  const char* src = static_cast<const char*>(a.q) + ((size_t)t * a.q_stride + lane * 8) * esz;
+  uint16_t* dst = a.q_out + (size_t)t * a.Hq * D + lane * 8;
+  auto load = [&](int h, uint4 (&v)[J][kVecs]) {
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int c0 = (lane + 32 * j) * 8;
+    for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[j][k] = 0.0f;
-      if (c0 < D && h < h1)
-        load8(a.q, a.q_f32 != 0, (size_t)t * a.q_stride + (size_t)h * D + c0, v[j]);
-    }
+      for (int k = 0; k < kVecs; ++k)
+        v[j][k] = h < h1 && (lane + 32 * j) * 8 < D
+                      ? __ldcs(reinterpret_cast<const uint4*>(
+                            src + ((size_t)h * D + 256 * j + 4 * k) * esz))
+                      : make_uint4(0, 0, 0, 0);
   };
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) load(h0 + warp + r * kWarps, y[r]);
-  float w[J][8];
+  for (int r = 0; r < kRows; ++r) load(h0 + warp + r * kWarps, raw[r]);
+  uint64_t w[J][4];
   const bool weighted = a.q_norm && a.q_weight != nullptr;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int c0 = (lane + 32 * j) * 8;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w[j][k] = weighted && c0 < D ? __ldg(a.q_weight + c0 + k) : 1.0f;
+    for (int k = 0; k < 4; ++k)
+      w[j][k] = weighted && c0 < D ? pack2(__ldg(a.q_weight + c0 + 2 * k),
+                                           __ldg(a.q_weight + c0 + 2 * k + 1))
+                                   : pack2(1.0f, 1.0f);
   }
   if (kPath != kNone) {
     const int pos = __ldg(a.pos + t);
@@ -334,39 +381,76 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     for (int r = 0; r < kRows; ++r) {
       const int hr = h + r * kWarps;
       if (hr >= h1) break;                             // the same for every lane
-      if (a.q_norm) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) sum = fmaf(y[r][j][k], y[r][j][k], sum);
-        const float f = 1.0f / sqrtf(warp_sum(sum) / D + a.eps);
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) y[r][j][k] *= f * w[j][k];
-      }
-      rotate_row<J, kPath>(a, y[r], strip, cs);
+      uint64_t y[J][4];
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const int c0 = (lane + 32 * j) * 8;
-        if (c0 < D)
-          __stcs(reinterpret_cast<uint4*>(a.q_out + ((size_t)t * a.Hq + hr) * D + c0),
-                 pack_bf16x8(y[r][j]));
+        if (kWide) {
+#pragma unroll
+          for (int k = 0; k < kVecs; ++k) {
+            const uint4 v = raw[r][j][k];
+            y[j][2 * k] = pack2(__uint_as_float(v.x), __uint_as_float(v.y));
+            y[j][2 * k + 1] = pack2(__uint_as_float(v.z), __uint_as_float(v.w));
+          }
+        } else {
+          const uint4 v = raw[r][j][0];
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            y[j][k] = pack2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u));
+        }
       }
-      load(hr + kRows * kWarps, y[r]);
+      load(hr + kRows * kWarps, raw[r]);
+      if (a.q_norm) {
+        uint64_t s2 = 0;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s2 = fma2(y[j][k], y[j][k], s2);
+        const float2 s = unpack2(s2);
+        // (rsqrtf is within 2 ulp; the divide and the square root cost 40 instructions a row)
+        const float f = rsqrtf(fmaf(warp_sum(s.x + s.y), inv_d, a.eps));
+        const uint64_t f2 = pack2(f, f);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[j][k] = mul2(mul2(y[j][k], f2), w[j][k]);
+      }
+      rotate_row<J, kPath>(a, y, strip, cs);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if ((lane + 32 * j) * 8 >= D) continue;
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = unpack2(y[j][k]);
+          o[k] = pack_bf162(v.x, v.y);
+        }
+        __stcs(reinterpret_cast<uint4*>(dst + (size_t)hr * D + 256 * j),
+               make_uint4(o[0], o[1], o[2], o[3]));
+      }
     }
   }
 }
 
-template <int J>
+template <int J, bool kWide>
 cudaError_t launch_j(int path, const NormRope& p, unsigned grid, size_t smem,
                      cudaStream_t stream) {
-  void (*kernel)(const NormRope) = path == kNone     ? norm_rope_kernel<J, kNone>
-                                   : path == kInLane ? norm_rope_kernel<J, kInLane>
-                                   : path == kExchange ? norm_rope_kernel<J, kExchange>
-                                                       : norm_rope_kernel<J, kStrip>;
+  void (*kernel)(const NormRope) = path == kNone     ? norm_rope_kernel<J, kNone, kWide>
+                                   : path == kInLane ? norm_rope_kernel<J, kInLane, kWide>
+                                   : path == kExchange ? norm_rope_kernel<J, kExchange, kWide>
+                                                       : norm_rope_kernel<J, kStrip, kWide>;
   return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, dim3(1), p);
+}
+
+template <bool kWide>
+cudaError_t launch_wide(int path, const NormRope& p, unsigned grid, size_t smem,
+                        cudaStream_t stream) {
+  switch (ceil_div(p.a.D, 256)) {
+    case 1: return launch_j<1, kWide>(path, p, grid, smem, stream);
+    case 2: return launch_j<2, kWide>(path, p, grid, smem, stream);
+    case 3: return launch_j<3, kWide>(path, p, grid, smem, stream);
+    default: return launch_j<4, kWide>(path, p, grid, smem, stream);
+  }
 }
 
 }  // namespace
@@ -400,19 +484,15 @@ cudaError_t launch_qk_norm_rope(const csa2_norm_rope_args& a, const fp4_kv_pages
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
   int path = kStrip;
   if (a.R == 0) path = kNone;
-  else if (a.interleaved && a.rot_begin % 2 == 0) path = kInLane;
+  else if (a.interleaved && a.rot_begin % 8 == 0 && a.R % 8 == 0) path = kInLane;
   else if (!a.interleaved && a.R % 16 == 0 && a.rot_begin % 8 == 0 &&
            a.rot_begin / 256 == (a.rot_begin + a.R - 1) / 256)
     path = kExchange;
   const size_t for_entries = a.E > 0 ? p.entries_per_cta * per_entry : 0;
   const size_t for_queries = (path == kStrip ? 1 + kWarps : 1) * (size_t)a.R * sizeof(float);
   const size_t smem = for_entries > for_queries ? for_entries : for_queries;
-  switch (ceil_div(a.D, 256)) {
-    case 1: return launch_j<1>(path, p, (unsigned)grid, smem, stream);
-    case 2: return launch_j<2>(path, p, (unsigned)grid, smem, stream);
-    case 3: return launch_j<3>(path, p, (unsigned)grid, smem, stream);
-    default: return launch_j<4>(path, p, (unsigned)grid, smem, stream);
-  }
+  return a.T > 0 && a.q_f32 ? launch_wide<true>(path, p, (unsigned)grid, smem, stream)
+                            : launch_wide<false>(path, p, (unsigned)grid, smem, stream);
 }
 
 }  // namespace csa2
