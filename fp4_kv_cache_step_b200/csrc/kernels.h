@@ -173,20 +173,13 @@ cudaError_t launch_pages_compact(const fp4_kv_pages& pg, int32_t* used, void* wo
 cudaError_t launch_qk_norm_rope(const csa2_norm_rope_args& a, const fp4_kv_pages* pages, int* err,
                                 cudaStream_t stream);
 
-// Attention over a paged cache (paged_attn.cu); see csa2_paged_attn. topk_idx
-// NULL: every visible entry.
+// Attention over a paged cache (paged_attn_tc.cu); see csa2_paged_attn. topk_idx
+// NULL (K 0): every visible entry.
 size_t paged_attn_workspace_bytes(const fp4_kv_pages& pg, int B, int Tq, int Hq, int K);
 cudaError_t launch_paged_attn(const uint16_t* q, const fp4_kv_pages& pg, const int32_t* seq,
                               const int32_t* nvalid, const int32_t* topk_idx, int B, int Tq,
                               int Hq, int K, float softmax_scale, uint16_t* out, float* lse,
                               void* workspace, int* err, cudaStream_t stream);
-
-// Its kernel over every visible entry (paged_attn_tc.cu).
-size_t paged_attn_dense_workspace_bytes(const fp4_kv_pages& pg, int B, int Tq, int Hq);
-cudaError_t launch_paged_attn_dense(const uint16_t* q, const fp4_kv_pages& pg, const int32_t* seq,
-                                    const int32_t* nvalid, int B, int Tq, int Hq,
-                                    float softmax_scale, uint16_t* out, float* lse,
-                                    void* workspace, int* err, cudaStream_t stream);
 
 // Tensor-core attention kernel (attn_tc.cu). With nsplit > 1 the splits are
 // merged inside the kernel (thread-block clusters, *merged set to true) when

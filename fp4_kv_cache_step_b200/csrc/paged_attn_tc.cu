@@ -1,5 +1,5 @@
-// paged_attn_tc.cu -- attention of a few query tokens over every visible entry of
-// a paged FP4 cache (csa2_paged_attn without a list), on the 5th-generation
+// paged_attn_tc.cu -- attention of a few query tokens over a paged FP4 cache
+// (csa2_paged_attn), every visible entry or a list of them, on the 5th-generation
 // tensor cores.
 //
 // One entry is key and value; all heads share it. The query rows of a sequence
@@ -21,8 +21,13 @@
 // one that is cut leaves fp16 partials with their (maximum, sum), which
 // paged_combine_kernel joins. A sequence without entries has one empty tile.
 //
+// With lists each query token is a sequence of its own here, its list the entries
+// (a place without an id takes its turn as an entry that is not there).
+//
 // Roles. Warp 15 copies rows (288 bytes each, contiguous within a page) to shared
-// memory, two tiles ahead. Warps 0-9 dequantise them (exact in fp16: at most 6
+// memory, two tiles ahead: bulk copies of a page's part of a tile, or with lists
+// 16-byte copies, 18 to a row (a bulk copy of one row costs about 58 cycles to
+// issue, 80 of them more than a tile's products). Warps 0-9 dequantise them (exact in fp16: at most 6
 // significant bits) into the tile, channels 0-255 first; 0-7 also stage the query
 // block. Warp 14 issues the MMAs, two tiles at a time: S S PV PV, so that the
 // softmax of one tile runs beside S of the next, and a tile is filled again while
@@ -120,7 +125,10 @@ struct Params {
   int shift;
   const int32_t* seq;
   const int32_t* nvalid;
-  int B, Tq, Hq, nblk;
+  const int32_t* ids;  // [B][K], or null for every entry
+  int K;
+  int B, Tq, Hq, nblk; // with lists B counts query tokens, and Tq is 1
+  int per_slot;        // query tokens to an entry of seq (with lists; else 1)
   float softmax_scale;
   uint16_t* out;
   float* lse;
@@ -303,9 +311,13 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) {
 }
 
 // ---------------------------------------------------------------- lengths, pieces
-// Entries that slot seq[b] holds (0 for a bad slot).
+__device__ __forceinline__ int slot_of(const Params& p, int b) {
+  return p.seq ? __ldg(p.seq + b / p.per_slot) : b / p.per_slot;
+}
+
+// Entries that b's slot holds (0 for a bad slot).
 __device__ __forceinline__ int slot_len(const Params& p, int b, bool tell) {
-  const int s = p.seq ? __ldg(p.seq + b) : b;
+  const int s = slot_of(p, b);
   if (s < 0 || s >= p.pg.S) {
     if (tell) record_error(p.err, CSA2_ERR_DEVICE_INDEX);
     return 0;
@@ -319,7 +331,7 @@ __device__ int visible(const Params& p, int b, int t) {
   return p.nvalid ? min(max(0, __ldg(p.nvalid + (size_t)b * p.Tq + t)), len) : len;
 }
 
-// ... that its queries see at most.
+// ... that b's queries see at most.
 __device__ int visible_most(const Params& p, int b, bool tell) {
   int lo = 0, hi = 0;
   if (p.nvalid) {
@@ -336,6 +348,12 @@ __device__ int visible_most(const Params& p, int b, bool tell) {
   if (!p.nvalid) return len;
   if (tell && (lo < 0 || hi > len)) record_error(p.err, CSA2_ERR_DEVICE_INDEX);
   return min(max(0, hi), len);
+}
+
+// Entries to go through for b: those its queries see at most, or its list's places.
+template <bool kListed>
+__device__ __forceinline__ int entries_of(const Params& p, int b, bool tell) {
+  return kListed ? p.K : visible_most(p, b, tell);
 }
 
 __device__ __forceinline__ int tiles_of(int n) { return max(1, (n + kT - 1) / kT); }
@@ -357,6 +375,7 @@ __device__ __forceinline__ int piece_of(long long unit, int pieces, long long to
 // Cuts the next segment off the piece: sm.seg[at] from its predecessor
 // sm.seg[at ^ 1] (whose b, or the one after it, is the sequence at sm.pos). One
 // thread. n_most: the sequence's visible entries where they are known, else -1.
+template <bool kListed>
 __device__ __noinline__ void next_segment(const Params& p, Smem& sm, int at, int n_most) {
   const Segment& prev = sm.seg[at ^ 1];
   Segment s;
@@ -373,7 +392,7 @@ __device__ __noinline__ void next_segment(const Params& p, Smem& sm, int at, int
       ++s.b;
     }
     const int pieces = (int)min((long long)gridDim.x, sm.total), piece = (int)blockIdx.x;
-    s.n_most = n_most >= 0 ? n_most : visible_most(p, s.b, false);
+    s.n_most = n_most >= 0 ? n_most : entries_of<kListed>(p, s.b, false);
     s.tiles = tiles_of(s.n_most);
     const int units = kSetup + s.tiles;
     s.blk = (int)quotient(pos - sm.base, units);
@@ -393,6 +412,7 @@ __device__ __noinline__ void next_segment(const Params& p, Smem& sm, int at, int
   sm.seg[at] = s;
 }
 
+template <bool kListed>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t vs[];   // [2][8 atoms][80 entries][128 B]
   uint8_t* ps = vs + 2 * kVTile;               // [2][64 rows][128 B], [2][64 rows][32 B]
@@ -407,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
     mbar_init(&sm.bar.o_full, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.bar.s_full[i], 1);
-      mbar_init(&sm.bar.raw_full[i], 1);
+      mbar_init(&sm.bar.raw_full[i], kListed ? 32 : 1);
       mbar_init(&sm.bar.v_free[i][0], 1);
       mbar_init(&sm.bar.v_free[i][1], 1);
     }
@@ -426,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
     long long mine = 0;
     int n_last = 0;
     for (int b = b0; b < b1; ++b) {
-      n_last = visible_most(p, b, blockIdx.x == 0);
+      n_last = entries_of<kListed>(p, b, blockIdx.x == 0);
       mine += (long long)p.nblk * pair_units(n_last);
     }
     sums[threadIdx.x] = mine;
@@ -455,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       long long at = before;
       int b = b0;
       for (; b + 1 < b1; ++b) {
-        const long long k = (long long)p.nblk * pair_units(visible_most(p, b, false));
+        const long long k = (long long)p.nblk * pair_units(entries_of<kListed>(p, b, false));
         if (begin < at + k) break;
         at += k;
       }
@@ -465,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       sm.seg[1].g0 = sm.seg[1].used0 = sm.seg[1].used1 = 0;
       sm.pos = begin;
       sm.end = (int)blockIdx.x < pieces ? piece_begin((int)blockIdx.x + 1, pieces, total) : begin;
-      next_segment(p, sm, 0, each == 1 ? n_last : -1);
+      next_segment<kListed>(p, sm, 0, each == 1 ? n_last : -1);
     }
   }
   tc_fence_before();
@@ -645,13 +665,89 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
         tile(t, 0);
         if (t + 1 < nt) tile(t + 1, 1);
       }
+    } else if (warp == kLoadWarp && kListed) {
+      // ---------------------------------------------------------- copies of listed rows
+      // Lane i has places i, i + 32 and i + 64 of a tile: their ids are loaded two
+      // tiles ahead, the table places of the ids one.
+      constexpr int kIds = 3;
+      const int t0 = S.t0;
+      const uint32_t g0 = S.g0;
+      const int s = slot_of(p, S.b);
+      const int n = visible_most(p, S.b, true);            // ids lie below
+      const int32_t* ids = p.ids + (size_t)S.b * p.K;
+      const int32_t* table = p.pg.table + (size_t)(n > 0 ? s : 0) * p.pg.M;
+      auto fetch_id = [&](int t, int k) -> int {
+        const int i = lane + 32 * k;
+        const long long e = (long long)(t0 + t) * kT + i;
+        if (t >= nt || i >= kT || e >= p.K) return -1;
+        return __ldg(ids + e);
+      };
+      auto check_id = [&](int id) -> int {
+        if (id >= -1 && id < n) return id;
+        record_error(p.err, CSA2_ERR_DEVICE_INDEX);
+        return -1;
+      };
+      auto fetch_place = [&](int id) { return id >= 0 ? __ldg(table + (id >> p.shift)) : 0; };
+      int id[kIds], place[kIds], id_next[kIds];
+#pragma unroll
+      for (int k = 0; k < kIds; ++k) {
+        id[k] = check_id(fetch_id(0, k));
+        place[k] = fetch_place(id[k]);
+        id_next[k] = fetch_id(1, k);
+      }
+      for (int t = 0; t < nt; ++t) {
+        const int buf = t & 1;
+        int row[kIds];
+        uint32_t bits[kIds];
+#pragma unroll
+        for (int k = 0; k < kIds; ++k) {
+          row[k] = -1;
+          if (id[k] >= 0) {
+            if (place[k] < 0 || place[k] >= p.pg.P)
+              record_error(p.err, CSA2_ERR_DEVICE_INDEX);
+            else
+              row[k] = (place[k] << p.shift) + (id[k] & (p.pg.page - 1));
+          }
+          bits[k] = __ballot_sync(0xffffffffu, row[k] >= 0);
+          id[k] = check_id(id_next[k]);
+          place[k] = fetch_place(id[k]);
+          id_next[k] = fetch_id(t + 2, k);
+        }
+        if (t >= 2) bar_sync(kBarV + 2 * buf + 1, kNumV1);     // the rows before are read
+        if (lane == 0) sm.valid[(g0 + t) & 3] = make_uint4(bits[0], bits[1], bits[2], 0);
+        const uint32_t dst = smem_u32(raw) + (uint32_t)(buf * kRawTile) + 16u * lane;
+#pragma unroll
+        for (int k = 0; k < kIds; ++k) {
+          // rows 32 k .. : 18 16-byte pieces each, dealt to the lanes in order
+          constexpr int kPieces = kRowBytes / 16;
+          const int rounds = k < 2 ? kPieces : (kT - 64) * kPieces / 32;
+#pragma unroll 6
+          for (int j = 0; j < rounds; ++j) {
+            const int x = 32 * j + lane, r = x / kPieces;
+            const int at = __shfl_sync(0xffffffffu, row[k], r);
+            if (at >= 0)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                               dst + (uint32_t)(32 * k * kRowBytes + 512 * j)),
+                           "l"(p.pg.rows + (size_t)at * kRowBytes + (x - r * kPieces) * 16)
+                           : "memory");
+          }
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                         smem_u32(&sm.bar.raw_full[buf]))
+                     : "memory");
+        __syncwarp();
+        bar_arrive(kBarL + buf, kNumL);
+      }
+      for (int t = max(0, nt - 2); t < nt; ++t)
+        bar_sync(kBarV + 2 * (t & 1) + 1, kNumV1);
+      if (lane == 0) next_segment<kListed>(p, sm, (int)(sph ^ 1), -1);
     } else if (warp == kLoadWarp) {
       // ---------------------------------------------------------- bulk copies
       // Lane i copies the rows of a tile that lie in its i-th page (a tile of 80
       // entries touches at most 11 pages of 8).
       const int n_most = S.n_most, t0 = S.t0;
       const uint32_t g0 = S.g0;
-      const int s = n_most > 0 ? (p.seq ? __ldg(p.seq + S.b) : S.b) : 0;
+      const int s = n_most > 0 ? slot_of(p, S.b) : 0;
       const int32_t* table = p.pg.table + (size_t)s * p.pg.M;
       // entries [lo, hi) of the sequence in lane i's page of tile t
       auto range = [&](int t, long long* lo, long long* hi) {
@@ -703,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       }
       for (int t = max(0, nt - 2); t < nt; ++t)
         bar_sync(kBarV + 2 * (t & 1) + 1, kNumV1);
-      if (lane == 0) next_segment(p, sm, (int)(sph ^ 1), -1);
+      if (lane == 0) next_segment<kListed>(p, sm, (int)(sph ^ 1), -1);
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMA issuer
       // The whole warp runs this with warp-uniform values and one elected lane
@@ -782,7 +878,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       const bool real = r0 + h < p.Tq * p.Hq;
       const float hs = real ? fabsf(p.softmax_scale) * kLog2e * sm.qdown[h] : 0.0f;
       // entries that this row sees from the segment's first on
-      const int n_row = (real && p.nvalid ? visible(p, S.b, (r0 + h) / p.Hq) : S.n_most) - S.t0 * kT;
+      const int n_row = (!kListed && real && p.nvalid ? visible(p, S.b, (r0 + h) / p.Hq) : S.n_most) -
+                        S.t0 * kT;
       const uint32_t g0 = S.g0, used0 = S.used0, used1 = S.used1;
       float m_ref = -INFINITY, l = 0.0f;
       bool ok = true;
@@ -965,7 +1062,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
 // many when each comes from few pieces (2280 rows of 4 to 9: four rows per CTA 5 us
 // less than one), and few when they come from many (256 rows of 37: one per CTA).
 template <int kGroups>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const Params p) {
+__global__ void __launch_bounds__(256) paged_combine_kernel(const Params p, int b0) {
   constexpr int kRowsPerCta = 4 / kGroups;
   __shared__ float part[kGroups][64][9];               // (kGroups > 1) 8 channels, weight
   pdl_wait_and_release();
@@ -973,7 +1070,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const Params p) {
   const int unit = threadIdx.x >> 6, grp = unit % kGroups;
   const int r = blockIdx.x * kRowsPerCta + unit / kGroups;         // row of the sequence
   if (r >= per_seq) return;
-  const size_t b = blockIdx.y;
+  const size_t b = (size_t)b0 + blockIdx.y;
   const int4 info = p.ws_info[b * p.nblk + r / kRows];
   const int first = info.x, last = info.y;
   if (first == last) return;
@@ -1029,7 +1126,7 @@ int sm_count_of_device() {
   return n;
 }
 
-// The kernel's shared memory, allowed once per device.
+// The kernels' shared memory, allowed once per device.
 cudaError_t allow_shared_memory() {
   static std::mutex mu;
   static bool done[64] = {};
@@ -1039,35 +1136,48 @@ cudaError_t allow_shared_memory() {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
   if (done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(paged_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)kSmemBytes);
+  e = cudaFuncSetAttribute(paged_attn_tc_kernel<false>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(paged_attn_tc_kernel<true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   done[dev] = e == cudaSuccess;
   return e;
 }
 
-// Pieces of the line of tiles: one per SM, never more than there can be units.
-int most_pieces(const fp4_kv_pages& pg, int B, int nblk) {
-  const long long units = kSetup + ((long long)pg.M * pg.page + kT - 1) / kT;
-  const long long all = units * B * nblk;
-  const int sms = sm_count_of_device();
-  return (int)(all < sms ? all : sms);
-}
+// What a call goes through: pairs of a sequence (with lists: a query token) and a
+// block of 64 of its rows, of at most `most` entries each.
+struct Shape {
+  int B, rows, nblk;
+  long long most;
+  Shape(const fp4_kv_pages& pg, int B_, int Tq, int Hq, int K)
+      : B(K ? B_ * Tq : B_), rows(K ? Hq : Tq * Hq), nblk(ceil_div(rows, kRows)),
+        most(K ? K : (long long)pg.M * pg.page) {}
+  // pieces of the line of tiles: one per SM, never more than there can be units
+  int pieces() const {
+    const long long all = (kSetup + (most + kT - 1) / kT) * B * nblk;
+    const int sms = sm_count_of_device();
+    return (int)(all < sms ? all : sms);
+  }
+};
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-size_t paged_attn_dense_workspace_bytes(const fp4_kv_pages& pg, int B, int Tq, int Hq) {
-  const int nblk = ceil_div(Tq * Hq, kRows);
-  const size_t slots = 2 * (size_t)most_pieces(pg, B, nblk);
-  return up256((size_t)B * nblk * sizeof(int4)) + up256(slots * kRows * sizeof(float2)) +
+size_t paged_attn_workspace_bytes(const fp4_kv_pages& pg, int B, int Tq, int Hq, int K) {
+  const Shape sh(pg, B, Tq, Hq, K);
+  const size_t slots = 2 * (size_t)sh.pieces();
+  return up256((size_t)sh.B * sh.nblk * sizeof(int4)) + up256(slots * kRows * sizeof(float2)) +
          slots * kRows * kD * sizeof(__half);
 }
 
-cudaError_t launch_paged_attn_dense(const uint16_t* q, const fp4_kv_pages& pg, const int32_t* seq,
-                                    const int32_t* nvalid, int B, int Tq, int Hq,
-                                    float softmax_scale, uint16_t* out, float* lse,
-                                    void* workspace, int* err, cudaStream_t stream) {
+cudaError_t launch_paged_attn(const uint16_t* q, const fp4_kv_pages& pg, const int32_t* seq,
+                              const int32_t* nvalid, const int32_t* topk_idx, int B, int Tq,
+                              int Hq, int K, float softmax_scale, uint16_t* out, float* lse,
+                              void* workspace, int* err, cudaStream_t stream) {
+  if (topk_idx == nullptr) K = 0;
+  const Shape sh(pg, B, Tq, Hq, K);
   Params p;
   p.q = q;
   p.pg = pg;
@@ -1075,30 +1185,41 @@ cudaError_t launch_paged_attn_dense(const uint16_t* q, const fp4_kv_pages& pg, c
   while ((1 << p.shift) < pg.page) ++p.shift;
   p.seq = seq;
   p.nvalid = nvalid;
-  p.B = B;
-  p.Tq = Tq;
+  p.ids = topk_idx;
+  p.K = K;
+  p.B = sh.B;
+  p.Tq = K ? 1 : Tq;
   p.Hq = Hq;
-  p.nblk = ceil_div(Tq * Hq, kRows);
+  p.nblk = sh.nblk;
+  p.per_slot = K ? Tq : 1;
   p.softmax_scale = softmax_scale;
   p.out = out;
   p.lse = lse;
-  const int pieces = most_pieces(pg, B, p.nblk);
+  const int pieces = sh.pieces();
   unsigned char* w = static_cast<unsigned char*>(workspace);
   p.ws_info = reinterpret_cast<int4*>(w);
-  w += up256((size_t)B * p.nblk * sizeof(int4));
+  w += up256((size_t)sh.B * sh.nblk * sizeof(int4));
   p.ws_ml = reinterpret_cast<float2*>(w);
   w += up256(2 * (size_t)pieces * kRows * sizeof(float2));
   p.ws_o = reinterpret_cast<__half*>(w);
   p.err = err;
   cudaError_t e = allow_shared_memory();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_attn_tc_kernel, dim3(pieces), dim3(kThreads), kSmemBytes, stream, dim3(1),
-                 p);
+  e = launch_pdl(K ? paged_attn_tc_kernel<true> : paged_attn_tc_kernel<false>, dim3(pieces),
+                 dim3(kThreads), kSmemBytes, stream, dim3(1), p);
   if (e != cudaSuccess) return e;
-  if ((long long)B * Tq * Hq <= 8 * sm_count_of_device())
-    return launch_pdl(paged_combine_kernel<4>, dim3(Tq * Hq, B), dim3(256), 0, stream, dim3(1), p);
-  return launch_pdl(paged_combine_kernel<1>, dim3(ceil_div(Tq * Hq, 4), B), dim3(256), 0, stream,
-                    dim3(1), p);
+  // rows in x, sequences in y (at most 65535 of each: y would not hold more)
+  const int rows = sh.rows;
+  for (int b0 = 0; b0 < sh.B; b0 += 65535) {
+    const unsigned nb = (unsigned)(sh.B - b0 < 65535 ? sh.B - b0 : 65535);
+    if ((long long)sh.B * rows <= 8 * sm_count_of_device())
+      e = launch_pdl(paged_combine_kernel<4>, dim3(rows, nb), dim3(256), 0, stream, dim3(1), p, b0);
+    else
+      e = launch_pdl(paged_combine_kernel<1>, dim3(ceil_div(rows, 4), nb), dim3(256), 0, stream,
+                     dim3(1), p, b0);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace csa2
