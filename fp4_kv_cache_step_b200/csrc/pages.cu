@@ -102,9 +102,11 @@ template <typename Sel, typename Put>
 __device__ void emit_pages(const int32_t* refs, int lo, int hi, int P, long long at,
                            long long limit, Sel sel, Put put) {
   const int lane = threadIdx.x & 31;
+  int4 next = lo < hi ? load_refs(refs, lo + 4 * lane, P) : make_int4(-1, -1, -1, -1);
   for (int p0 = lo; p0 < hi && at < limit; p0 += 128) {
     const int p = p0 + 4 * lane;
-    const int4 r = load_refs(refs, p, P);
+    const int4 r = next;
+    if (p0 + 128 < hi) next = load_refs(refs, p + 128, P);   // on its way during this round
     const int rr[4] = {r.x, r.y, r.z, r.w};
     int mine = 0;
 #pragma unroll
@@ -325,25 +327,30 @@ __device__ __forceinline__ bool read_pair(const fp4_kv_pages& pg, int shift, int
 }
 
 // Reads pair i's source as it is before the call and takes the new references
-// (before any is given back, so that no page is free in between).
-__device__ void fork_stage(const fp4_kv_pages& pg, int shift, int a, bool ok, int len, int old_len,
-                           const ForkPlan& plan, int i, int tid, int threads, int* err) {
+// (before any is given back, so that no page is free in between). A place of the
+// destination that holds the source's page already keeps its reference: branches of
+// one prompt, forked again from each other, share most of theirs.
+__device__ void fork_stage(const fp4_kv_pages& pg, int shift, int a, int b, bool ok, int len,
+                           int old_len, const ForkPlan& plan, int i, int tid, int threads,
+                           int* err) {
   if (tid == 0) {
     if (!ok) record_error(err, CSA2_ERR_DEVICE_INDEX);
     plan.new_len[i] = ok ? len : -1;
     plan.old_len[i] = old_len;
   }
   if (!ok) return;
-  const int np = pages_for(len, shift);
+  const int np = pages_for(len, shift), old = pages_for(old_len, shift);
   const int32_t* row = pg.table + (size_t)a * pg.M;
+  const int32_t* had = pg.table + (size_t)b * pg.M;
   int32_t* to = plan.staged + (size_t)i * pg.M;
 #pragma unroll 4
   for (int j = tid; j < np; j += threads) {
     int p = row[j];
+    const int o = j < old ? had[j] : -1;
     if (p < 0 || p >= pg.P) {
       record_error(err, CSA2_ERR_DEVICE_INDEX);
       p = -1;
-    } else {
+    } else if (p != o) {
       atomicAdd(&pg.refs[p], 1);
     }
     to[j] = p;
@@ -359,11 +366,10 @@ __device__ void fork_apply(const fp4_kv_pages& pg, int shift, int b, const ForkP
   const int32_t* from = plan.staged + (size_t)i * pg.M;
 #pragma unroll 4
   for (int j = tid; j < max(np, old); j += threads) {
-    if (j < old) {
-      const int p = row[j];
-      if (p >= 0 && p < pg.P) atomicSub(&pg.refs[p], 1);
-    }
-    row[j] = j < np ? from[j] : -1;
+    const int p = j < old ? row[j] : -1, to = j < np ? from[j] : -1;
+    if (j < old && p == to) continue;
+    if (p >= 0 && p < pg.P) atomicSub(&pg.refs[p], 1);
+    row[j] = to;
   }
   if (tid == 0) pg.len[b] = len;
 }
@@ -373,11 +379,11 @@ __global__ void __launch_bounds__(kThreads)
 fork_stage_kernel(const fp4_kv_pages pg, int shift, const int32_t* __restrict__ src,
                   const int32_t* __restrict__ dst, int n, const ForkPlan plan, int* err) {
   pdl_wait_and_release();
-  const int i = blockIdx.x, a = src[i];
+  const int i = blockIdx.x, a = src[i], b = dst[i];
   int len, old_len;
-  bool ok = read_pair(pg, shift, a, dst[i], &len, &old_len);
+  bool ok = read_pair(pg, shift, a, b, &len, &old_len);
   ok = __syncthreads_or(listed_again(dst, n, i, threadIdx.x, kThreads)) == 0 && ok;
-  fork_stage(pg, shift, a, ok, len, old_len, plan, i, blockIdx.y * kThreads + threadIdx.x,
+  fork_stage(pg, shift, a, b, ok, len, old_len, plan, i, blockIdx.y * kThreads + threadIdx.x,
              gridDim.y * kThreads, err);
 }
 
@@ -399,11 +405,11 @@ fork_small_kernel(const fp4_kv_pages pg, int shift, const int32_t* __restrict__ 
   // (warps in turn over the CTAs, so that few pairs use all of them)
   const int w = (threadIdx.x >> 5) * kPlanCtas + (int)cl.block_rank();
   for (int i = w; i < n; i += kPlanWarps) {
-    const int a = src[i];
+    const int a = src[i], b = dst[i];
     int len, old_len;
-    bool ok = read_pair(pg, shift, a, dst[i], &len, &old_len);
+    bool ok = read_pair(pg, shift, a, b, &len, &old_len);
     ok = !__any_sync(0xffffffffu, listed_again(dst, n, i, lane, 32)) && ok;
-    fork_stage(pg, shift, a, ok, len, old_len, plan, i, lane, 32, err);
+    fork_stage(pg, shift, a, b, ok, len, old_len, plan, i, lane, 32, err);
   }
   cl.sync();
   for (int i = w; i < n; i += kPlanWarps) fork_apply(pg, shift, dst[i], plan, i, lane, 32);
