@@ -559,7 +559,8 @@ CSA2_API csa2_status csa2_qk_norm_rope(const csa2_norm_rope_args* args, const fp
  *   workspace  csa2_paged_attn_workspace_bytes() bytes (K 0 without topk_idx);
  *              not shared by calls that may overlap
  * A slot outside [0, S) is recorded and has no entries, and neither has a table
- * place that holds no page. Requires pages->D == 512, 1 <= Hq, Tq >= 0,
+ * place that holds no page. Scale bytes of the rows that are read must not be NaN
+ * (0x7f, 0xff; no call of this library writes one). Requires pages->D == 512, 1 <= Hq, Tq >= 0,
  * Tq * Hq <= 65535, B <= 65535.
  * ------------------------------------------------------------------------ */
 CSA2_API size_t csa2_paged_attn_workspace_bytes(const fp4_kv_pages* pages, int B, int Tq, int Hq,

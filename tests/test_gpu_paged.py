@@ -186,6 +186,30 @@ def test_large_pool_and_many_slots():
     assert errors() == "OK"
 
 
+@pytest.mark.parametrize("page,D,S,M", [(64, 512, 9, 7), (128, 512, 5, 4), (8, 128, 300, 100),
+                                        (16, 640, 40, 700)])
+def test_large_pages_and_long_tables(page, D, S, M):
+    """Copies in several pieces, and lists too long for one cluster's launch."""
+    r = np.random.RandomState(page)
+    P = S * M // 2 + 40
+    m, g = caches(P, page, D, S, M, seed=7)
+    half = S // 2
+    resize(m, g, np.arange(half), r.randint(0, M * page // 2, half))
+    dst = half + r.permutation(S - half)
+    fork(m, g, r.randint(0, half, S - half), dst)
+    same(m, g)
+    every = r.permutation(S)
+    resize(m, g, every, np.minimum(m.length[every] + r.randint(0, 4, S), M * page))
+    same(m, g)
+    fork(m, g, r.randint(0, S, half), np.arange(half))      # some places keep their page
+    resize(m, g, r.permutation(S)[: S // 3], r.randint(0, page, S // 3))
+    same(m, g)
+    csa2.fp4_kv_pages_compact(g)
+    m.compact()
+    same(m, g)
+    assert errors() == "OK" and not m.no_pages
+
+
 def test_upkeep_in_a_graph():
     """A captured fork + resize replayed: the second replay gives back what the first took."""
     m, g = caches(64, 8, 128, 4, 4)
@@ -373,7 +397,7 @@ def check_attn(m, slots, q, got, lse, scale, nvalid=None, ids=None):
             else:
                 # logits: 512 exact products added in fp32 (2^-24 of the sum of magnitudes per
                 # addition, a few dozen of them deep), exp2 and log2 to 2^-22
-                mag = np.abs(q[b, t]).dot(np.abs(sel).T).max() * scale
+                mag = np.abs(q[b, t]).dot(np.abs(sel).T).max() * abs(scale)
                 assert np.all(np.abs(lse[b, t] - wl) <= 2.0 ** -18 * (1 + mag)), (b, t)
 
 
@@ -401,6 +425,68 @@ def test_dense_with_sharp_softmax(scale):
     m, g, slots, q = attn_case(2, 1, 64, [1500, 700], 16, seed=9)
     out, lse = csa2.csa2_paged_attn(q, g, scale, seq=i32(slots))
     check_attn(m, slots, q, out, lse, scale)
+    assert errors() == "OK"
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+def test_scales_that_are_not_positive(scale):
+    """Scale 0: the mean of the visible values; a negative one turns the order round."""
+    m, g, slots, q = attn_case(2, 2, 40, [400, 81], 16, seed=6)
+    nv = np.array([[399, 400], [3, 81]])
+    out, lse = csa2.csa2_paged_attn(q, g, scale, seq=i32(slots), nvalid=i32(nv))
+    check_attn(m, slots, q, out, lse, scale, nvalid=nv)
+    assert errors() == "OK"
+
+
+def test_rows_behind_the_length_are_not_read():
+    """Free pages and the places behind a sequence's end hold NaN scales."""
+    m, g, slots, q = attn_case(3, 1, 64, [100, 1, 165], 16, seed=12)
+    held = np.zeros((m.P, m.page), bool)
+    for s in slots:
+        at = np.arange(m.length[s])
+        held[m.table[s, at // m.page], at % m.page] = True
+    m.rows[~held] = 0xff
+    g.rows.copy_(dev(m.rows))
+    out, lse = csa2.csa2_paged_attn(q, g, 0.05, seq=i32(slots))
+    check_attn(m, slots, q, out, lse, 0.05)
+    ids = np.array([[[0, 99, -1]], [[-1, 0, -1]], [[5, 6, 164]]])
+    out, lse = csa2.csa2_paged_attn(q, g, 0.05, seq=i32(slots), topk_idx=i32(ids))
+    check_attn(m, slots, q, out, lse, 0.05, ids=ids)
+    assert errors() == "OK"
+
+
+def test_pools_beyond_four_gigabytes():
+    """Pages whose bytes lie past 2^32: written, read, copied and moved."""
+    P, page, D, M = 240000, 64, 512, 3                      # 4.4 GB
+    if torch.cuda.get_device_properties(0).total_memory < 16 << 30:
+        pytest.skip("needs 16 GB")
+    g = csa2.Fp4Pages(torch.empty((P, page, 288), dtype=torch.uint8, device="cuda"),
+                      torch.full((2, M), -1, dtype=torch.int32, device="cuda"),
+                      torch.zeros(2, dtype=torch.int32, device="cuda"),
+                      torch.ones(P, dtype=torch.int32, device="cuda"))
+    g.refs[P - 5:] = 0                                      # the only free pages
+    csa2.fp4_kv_pages_resize(g, i32([0]), i32([100]))
+    assert g.table[0].tolist() == [P - 5, P - 4, -1]
+    x = bf16(np.random.RandomState(0).standard_normal((100, D)))
+    csa2.csa2_qk_norm_rope(csa2.csa2_rope_turns(0), 0, kv=x.cuda(), kv_pos=i32([0] * 100),
+                           kv_norm=False, pages=g, seq=i32([0] * 100), entry=i32(range(100)))
+    rows, vals = pm.quantise(x.double().numpy())
+    np.testing.assert_array_equal(g.rows[P - 5].cpu().numpy(), rows[:64])
+    q = bf16(np.random.RandomState(1).standard_normal((1, 1, 16, D))).cuda()
+    want, _ = pm.attention(q[0, 0].double().cpu().numpy(), vals, 0.05)
+    bound = 2.0 ** -9 * np.abs(vals).max()
+    for ids in (None, i32([[list(range(100))]])):
+        out, _ = csa2.csa2_paged_attn(q, g, 0.05, seq=i32([0]), topk_idx=ids)
+        err = np.abs(out[0, 0].double().cpu().numpy() - want)
+        assert np.all(err <= 0.5 * bf16_ulp(np.abs(want) + bound) + bound)
+    csa2.fp4_kv_pages_fork(g, i32([0]), i32([1]))
+    csa2.fp4_kv_pages_resize(g, i32([1]), i32([101]))       # 36 rows to page P - 3
+    assert g.table[1].tolist() == [P - 5, P - 3, -1]
+    np.testing.assert_array_equal(g.rows[P - 3, :36].cpu().numpy(), rows[64:])
+    g.refs[: P - 5] = 0                                     # three pages left in use
+    csa2.fp4_kv_pages_compact(g)
+    assert g.table.tolist() == [[0, 1, -1], [0, 2, -1]]
+    np.testing.assert_array_equal(g.rows[:2].flatten(0, 1)[:100].cpu().numpy(), rows)
     assert errors() == "OK"
 
 
