@@ -538,6 +538,16 @@ class Fp4Pages:
         self._c = PagesStruct(rows.data_ptr(), table.data_ptr(), length.data_ptr(),
                               refs.data_ptr(), P, page, self.D, S, M)
         self.ref = ctypes.byref(self._c)
+        self._sizes = {}
+
+    def workspace_bytes(self, call: str, *shape: int) -> int:
+        """Workspace of a paged call for a shape (asked once per shape)."""
+        need = self._sizes.get((call, shape))
+        if need is None:
+            with torch.cuda.device(self.index):
+                need = getattr(load(), call + "_workspace_bytes")(self.ref, *shape)
+            self._sizes[call, shape] = need
+        return need
 
     @classmethod
     def empty(cls, P: int, page: int, D: int, S: int, M: int, device="cuda") -> "Fp4Pages":
@@ -555,7 +565,7 @@ def fp4_kv_pages_resize(pages: Fp4Pages, seq: torch.Tensor, new_len: torch.Tenso
     grows is copied. Length 0 frees a slot."""
     n, index = seq.numel(), pages.index
     a, b = _vec(seq, "seq", _I32, n, index), _vec(new_len, "new_len", _I32, n, index)
-    ws, p, size = _scratch(workspace, load().fp4_kv_pages_resize_workspace_bytes(pages.ref, n),
+    ws, p, size = _scratch(workspace, pages.workspace_bytes("fp4_kv_pages_resize", n),
                            pages.device)
     _call("fp4_kv_pages_resize", index, pages.ref, a, b, n, p, size)
 
@@ -566,7 +576,7 @@ def fp4_kv_pages_fork(pages: Fp4Pages, src: torch.Tensor, dst: torch.Tensor,
     are shared, what dst[i] held is given back."""
     n, index = src.numel(), pages.index
     a, b = _vec(src, "src", _I32, n, index), _vec(dst, "dst", _I32, n, index)
-    ws, p, size = _scratch(workspace, load().fp4_kv_pages_fork_workspace_bytes(pages.ref, n),
+    ws, p, size = _scratch(workspace, pages.workspace_bytes("fp4_kv_pages_fork", n),
                            pages.device)
     _call("fp4_kv_pages_fork", index, pages.ref, a, b, n, p, size)
 
@@ -575,7 +585,7 @@ def fp4_kv_pages_compact(pages: Fp4Pages, used: Optional[torch.Tensor] = None,
                          workspace: Optional[torch.Tensor] = None) -> None:
     """Move the U pages in use to the places [0, U); used int32 [1] receives U."""
     u = None if used is None else _vec(used, "used", _I32, 1, pages.index)
-    ws, p, size = _scratch(workspace, load().fp4_kv_pages_compact_workspace_bytes(pages.ref),
+    ws, p, size = _scratch(workspace, pages.workspace_bytes("fp4_kv_pages_compact"),
                            pages.device)
     _call("fp4_kv_pages_compact", pages.index, pages.ref, u, p, size)
 
@@ -724,7 +734,7 @@ def csa2_paged_attn(q: torch.Tensor, pages: Fp4Pages, softmax_scale: float,
             raise ValueError("lse must be [B][Tq][Hq]")
         p_lse = _vec(lse, "lse", _F32, B * Tq * H, index)
     ws, p, size = _scratch(workspace,
-                           load().csa2_paged_attn_workspace_bytes(pages.ref, B, Tq, H, K), device)
+                           pages.workspace_bytes("csa2_paged_attn", B, Tq, H, K), device)
     _call("csa2_paged_attn", index, p_q, pages.ref, p_seq, p_nv, p_ids, B, Tq, H, K,
           softmax_scale, _vec(out, "out", _BF16, B * Tq * H * D, index), p_lse, p, size)
     return out, (lse if want_lse else None)

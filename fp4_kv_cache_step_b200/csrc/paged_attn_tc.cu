@@ -27,19 +27,30 @@
 // Roles. Warp 15 copies rows (288 bytes each, contiguous within a page) to shared
 // memory, two tiles ahead: bulk copies of a page's part of a tile, or with lists
 // 16-byte copies, 18 to a row (a bulk copy of one row costs about 58 cycles to
-// issue, 80 of them more than a tile's products). Warps 0-9 dequantise them (exact in fp16: at most 6
-// significant bits) into the tile, channels 0-255 first; 0-7 also stage the query
-// block. Warp 14 issues the MMAs, two tiles at a time: S S PV PV, so that the
-// softmax of one tile runs beside S of the next, and a tile is filled again while
-// the other is multiplied. Warps 10-13 run the softmax, a thread having half of one
-// row's entries. The reference maximum is lazy (raised, with O rescaled, only by a
-// logit more than 8 above it in log2 units), so P stays below 2^8 in fp16. All
+// issue, 80 of them more than a tile's products). Warps 0-9 dequantise them (exact
+// in fp16: at most 6 significant bits) into the tile, channels 0-255 first; 0-7 also
+// stage the query block. Warp 14 issues the MMAs, two tiles at a time: S S PV PV, so
+// that the softmax of one tile runs beside S of the next, and a tile is filled again
+// while the other is multiplied. Warps 10-13 run the softmax, a thread having half
+// of one row's entries. The reference maximum is lazy (raised, with O rescaled, only
+// by a logit more than 8 above it in log2 units), so P stays below 2^8 in fp16. All
 // sums are fp32.
 // Warps hand work to each other through named barriers, which cost tens of cycles
 // where a waiting mbarrier's wake-up beside this shared-memory load cost 500 to
 // 800; what the tensor core or the copy engine signals are mbarriers, every wait
 // on one of which is bounded. Named barriers need no bound: each role passes every
 // one of them for every tile, whether or not a wait before it ran out.
+//
+// What bounds it: the tensor core. An instruction of M = 64, K = 16 takes 47 cycles
+// at N = 80 (and at any N up to 96: the least there is) and 129 at N = 256, so a tile
+// costs 32 x 47 + 10 x 129 = 2794 cycles; measured 2865 (ncu: the tensor pipe active
+// 79 % of the kernel on 32 sequences of 16384 to 32768 entries, 64 heads, 138 us).
+// M = 64 leaves half of the array idle; 128 rows of O would be all of tensor memory.
+// Larger tiles would cost less per entry (96 entries: 32.3 cycles instead of 35), but
+// two of them leave no room for the rows to come. Shared memory is the next bound:
+// about 32 cycles per entry for filling a tile, reading it twice and staging rows.
+// Before and after its tiles a CTA spends about 10 us (plan 2.7, query block and
+// first tile 3.5, output 2.3).
 #include <mutex>
 
 #include "common.cuh"
@@ -1006,7 +1017,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
     tc_fence_before();
     const bool stop = __syncthreads_or(*abort_flag) != 0;
     tc_fence_after();
-    if (stop) break;
+    if (stop) {
+      // a wait ran out: what was copied may still be on its way (waited for again,
+      // for a limited time)
+      if (threadIdx.x == 0) {
+        int none = 0;
+        mbar_wait(&sm.bar.q_ld, sph, &none);
+        for (int i = 0; i < 2 && i < nt; ++i) {
+          none = 0;
+          const uint32_t last = (i ? S.used1 : S.used0) + (uint32_t)((nt - 1 - i) >> 1);
+          mbar_wait(&sm.bar.raw_full[i], last & 1, &none);
+        }
+      }
+      break;
+    }
     {
       const int r0 = S.blk * kRows, slot = S.slot;
       const int nr = min(kRows, p.Tq * p.Hq - r0);

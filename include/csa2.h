@@ -390,7 +390,8 @@ CSA2_API csa2_status csa2_layer_step(const csa2_layer_args* args, csa2_mode mode
  *   refs   int32 [P]
  * Requires page a power of two in [8, 65536], D % 128 == 0, D <= 1024,
  * 1 <= S <= 65536, M >= 1, P >= 1, M * page and P * page below 2^31, and every
- * pointer 16-byte aligned.
+ * pointer 16-byte aligned. Calls on one cache that may overlap (on several
+ * streams) must not change it, and no two such calls share a workspace.
  * ------------------------------------------------------------------------ */
 typedef struct {
   uint8_t* rows;
@@ -509,7 +510,8 @@ CSA2_API csa2_status csa2_rope_turns(int R, double base, csa2_rope_scaling scali
  *   kv_pos, seq, entry  int32 [E]
  *   kv_weight float [D]     NULL for ones; ignored without kv_norm
  *   kv_out    bf16 [E][D]   optional (NULL to skip): the values that the row
- *                           stands for (exact in bf16), also of a skipped entry
+ *                           stands for (exact in bf16), also of a skipped entry;
+ *                           apart from the inputs
  * A negative position is recorded (CSA2_ERR_DEVICE_INDEX) and turned the other way.
  * A NaN or infinity in kv, after its norm and rotation, is recorded
  * (CSA2_ERR_NONFINITE; the row is still written); in q it is passed on.
@@ -551,13 +553,13 @@ CSA2_API csa2_status csa2_qk_norm_rope(const csa2_norm_rope_args* args, const fp
  *   nvalid   int32 [B][Tq]   entries [0, nvalid) are visible; NULL: the slot's
  *                            length. One outside [0, len] is recorded
  *                            (CSA2_ERR_DEVICE_INDEX) and clamped to it
- *   topk_idx int32 [B][Tq][K]   ids in [-1, nvalid), -1 skipped, others
- *                            recorded and skipped; NULL (K ignored) for all
+ *   topk_idx int32 [B][Tq][K]   ids in [-1, nvalid) in any order, -1 skipped,
+ *                            others recorded and skipped, an id listed twice
+ *                            counted twice; NULL (K ignored) for all
  *   out      uint16 [B][Tq][Hq][D]  bf16
  *   lse      float  [B][Tq][Hq]     optional, natural log; no entry gives
  *                            out = 0 and lse = -inf
  *   workspace  csa2_paged_attn_workspace_bytes() bytes (K 0 without topk_idx);
- *              not shared by calls that may overlap
  * A slot outside [0, S) is recorded and has no entries, and neither has a table
  * place that holds no page. Scale bytes of the rows that are read must not be NaN
  * (0x7f, 0xff; no call of this library writes one). Requires pages->D == 512, 1 <= Hq, Tq >= 0,

@@ -510,6 +510,14 @@ def test_listed_entries(B, Tq, H, lens, page, K):
     assert errors() == "OK"
 
 
+def test_lists_in_any_order_with_repeats():
+    m, g, slots, q = attn_case(1, 1, 16, [300], 16, seed=5)
+    ids = np.array([[[299, 7, 7, -1, 0, 150, 7, -1, 31, 32]]])
+    out, lse = csa2.csa2_paged_attn(q, g, 0.05, seq=i32(slots), topk_idx=i32(ids))
+    check_attn(m, slots, q, out, lse, 0.05, ids=ids)        # an id counts as often as listed
+    assert errors() == "OK"
+
+
 def test_slots_in_order_and_without_lse():
     m, g, slots, q = attn_case(2, 1, 16, [50, 130], 16)
     every = q[:1].expand(4, 1, 16, 512).contiguous()        # rows 0 .. 3 read slots 0 .. 3
