@@ -13,13 +13,15 @@
 // chunks of 8 channels (lane + 32 j), read as 16-byte words, two heads at a time;
 // the weights stay in its registers and the cosines and sines of a token are
 // computed once per CTA, while the first heads are on their way. Rotation:
-//   neighbouring channels are in one lane's chunk, where the rotary part is whole chunks;
+//   neighbouring channels are in one lane's chunk (the first an even one);
 //   halves R/2 apart are R/16 chunks apart: one exchange between lanes, where
 //   the rotary part lies within one round of 32 chunks on chunk borders;
 //   anything else goes through a per-warp strip of shared memory.
 // An entry's group of 16 channels is two neighbouring lanes: one exchange gives its
 // maximum, the codes of a lane are one 32-bit word. Bound: HBM (a few dozen
-// instructions per 16 bytes read and written); at single tokens, the launch.
+// instructions per 16 bytes read and written); at single tokens, the launch. Measured:
+// 4096 tokens of 64 heads of 512 channels (bf16) and 1024 entries, 539 MB, in 94 to
+// 98 us, 5.5 to 5.7 TB/s (a plain copy: 6.5).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -29,7 +31,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 
-enum : int { kNone = 0, kInLane = 1, kExchange = 2, kStrip = 3 };   // how channels rotate
+// how channels rotate (kPairs: kInLane where the rotary part is not whole chunks)
+enum : int { kNone = 0, kInLane = 1, kPairs = 2, kExchange = 3, kStrip = 4 };
 
 // Two floats in one 64-bit register: half the instructions of separate ones.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -58,7 +61,8 @@ struct NormRope {
   fp4_kv_pages pg;
   int shift;
   int entry_blocks, entries_per_cta;
-  int q_blocks;      // CTAs per token's heads
+  int q_blocks;      // CTAs per token's heads, or 0: tokens_per_cta tokens of few heads
+  int tokens_per_cta;
   int heads_per_cta;
   int* err;
 };
@@ -95,12 +99,6 @@ __device__ __forceinline__ long long turn_fraction(int p, uint64_t t) {
   return (long long)((uint64_t)(long long)p * t);
 }
 
-// The channels of the rotary part that pair i joins.
-__device__ __forceinline__ void pair_of(const csa2_norm_rope_args& a, int i, int* u, int* v) {
-  *u = a.interleaved ? 2 * i : i;
-  *v = a.interleaved ? 2 * i + 1 : i + a.R / 2;
-}
-
 template <typename F>
 __device__ __forceinline__ F warp_sum(F x) {
 #pragma unroll
@@ -108,38 +106,43 @@ __device__ __forceinline__ F warp_sum(F x) {
   return x;
 }
 
-// Moves the rotary channels of a row held as chunks through `strip`: f64 or f32.
+// Place of channel c in a strip: one word of 33 skipped, as the lanes are 8 channels apart.
+__host__ __device__ constexpr int strip_at(int c) { return c + (c >> 5); }
+
+// Rotates through `strip` (by channel, strip_at(D) values of the warp): the chunks that
+// hold rotary channels go there, a lane takes every 32nd pair, and the chunks come back.
+// (Each lane rotating its own channels from there takes 1.15 to 1.45 times as long.)
 template <int J, typename F>
-__device__ __forceinline__ void rotate(const csa2_norm_rope_args& a, F (&y)[J][8], F* strip,
-                                       const F* cs) {
+__device__ __forceinline__ void rotate_strip(const csa2_norm_rope_args& a, F (&y)[J][8], F* strip,
+                                             const F* cs) {
   const int lane = threadIdx.x & 31;
-  const int b = a.rot_begin, R = a.R;
+  const int b = a.rot_begin, end = b + a.R, half = a.R / 2;
+  const int next = a.interleaved ? 2 : 1, other = a.interleaved ? 1 : half;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int c0 = (lane + 32 * j) * 8;
-    if (c0 < a.D && c0 + 8 > b && c0 < b + R) {
+    if (c0 >= a.D || c0 + 8 <= b || c0 >= end) continue;
+    F* at = strip + strip_at(c0);                      // a chunk lies within one run of 32
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c0 + k >= b && c0 + k < b + R) strip[c0 + k - b] = y[j][k];
-    }
+    for (int k = 0; k < 8; ++k) at[k] = y[j][k];
   }
   __syncwarp();
-  for (int i = lane; i < R / 2; i += 32) {
-    int u, v;
-    pair_of(a, i, &u, &v);
-    const F x0 = strip[u], x1 = strip[v], c = cs[2 * i], s = cs[2 * i + 1];
-    strip[u] = x0 * c - x1 * s;
-    strip[v] = x1 * c + x0 * s;
+  for (int i = lane; i < half; i += 32) {
+    const int c = b + i * next;
+    F* pu = strip + strip_at(c);
+    F* pv = strip + strip_at(c + other);
+    const F u = *pu, v = *pv, co = cs[2 * i], si = cs[2 * i + 1];
+    *pu = u * co - v * si;
+    *pv = v * co + u * si;
   }
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int c0 = (lane + 32 * j) * 8;
-    if (c0 < a.D && c0 + 8 > b && c0 < b + R) {
+    if (c0 >= a.D || c0 + 8 <= b || c0 >= end) continue;
+    const F* at = strip + strip_at(c0);
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c0 + k >= b && c0 + k < b + R) y[j][k] = strip[c0 + k - b];
-    }
+    for (int k = 0; k < 8; ++k) y[j][k] = at[k];
   }
   __syncwarp();
 }
@@ -165,7 +168,7 @@ __device__ __forceinline__ uint32_t e4m3_code64(double x) {
   return (uint32_t)((e + 6) * 8 + n);                  // n = 16 carries into the exponent
 }
 
-template <int J>
+template <int J, int kPath>
 __device__ void entry_row(const NormRope& p, int e, double* strip, const double* cs) {
   const csa2_norm_rope_args& a = p.a;
   const int lane = threadIdx.x & 31;
@@ -194,7 +197,21 @@ __device__ void entry_row(const NormRope& p, int e, double* strip, const double*
         y[j][k] *= a.kv_weight ? r * (double)__ldg(a.kv_weight + c0 + k) : r;
     }
   }
-  if (a.R) rotate<J>(a, y, strip, cs);
+  if (kPath == kInLane || kPath == kPairs) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int c0 = (lane + 32 * j) * 8 - a.rot_begin;     // in the rotary part; even
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        if (c0 + k < 0 || c0 + k >= a.R) continue;
+        const double u = y[j][k], v = y[j][k + 1], c = cs[c0 + k], s = cs[c0 + k + 1];
+        y[j][k] = u * c - v * s;
+        y[j][k + 1] = v * c + u * s;
+      }
+    }
+  } else if (kPath != kNone) {
+    rotate_strip<J>(a, y, strip, cs);
+  }
 
   // the row in the cache: its slot's page must be this slot's alone
   const int s = __ldg(a.seq + e), at = __ldg(a.entry + e);
@@ -263,6 +280,19 @@ __device__ __forceinline__ void rotate_row(const csa2_norm_rope_args& a, uint64_
         y[j][k] = pack2(v.x * c[k] - v.y * s[k], v.y * c[k] + v.x * s[k]);
       }
     }
+  } else if (kPath == kPairs) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int c0 = (lane + 32 * j) * 8 - b;          // in the rotary part; even
+      if (c0 <= -8 || c0 >= R) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (c0 + 2 * k < 0 || c0 + 2 * k >= R) continue;
+        const float2 t = *reinterpret_cast<const float2*>(cs + c0 + 2 * k);
+        const float2 v = unpack2(y[j][k]);
+        y[j][k] = pack2(v.x * t.x - v.y * t.y, v.y * t.x + v.x * t.y);
+      }
+    }
   } else if (kPath == kExchange) {
     const int jr = b >> 8, first = (b >> 3) & 31, half = R >> 4;   // in chunks
 #pragma unroll
@@ -293,7 +323,7 @@ __device__ __forceinline__ void rotate_row(const csa2_norm_rope_args& a, uint64_
         x[j][2 * k] = v.x;
         x[j][2 * k + 1] = v.y;
       }
-    rotate<J>(a, x, strip, cs);
+    rotate_strip<J>(a, x, strip, cs);
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -302,20 +332,24 @@ __device__ __forceinline__ void rotate_row(const csa2_norm_rope_args& a, uint64_
 }
 
 // CTAs [0, entry_blocks) take entries, one per warp (they come first, being the
-// longest chains); the others heads_per_cta heads of a token.
+// longest chains); the others heads_per_cta heads of a token, or all heads of
+// tokens_per_cta tokens, a row per warp.
 // (64 registers a thread where they suffice: 32 warps per SM, 2 KB each in flight)
 template <int J, int kPath, bool kWide>
-__global__ void __launch_bounds__(kThreads, J <= 2 ? 4 : 2) norm_rope_kernel(const __grid_constant__ NormRope p) {
-  // queries: cosines and sines of the R/2 pairs, then a strip of R floats per warp;
-  // entries: per warp both as doubles
+__global__ void __launch_bounds__(kThreads, J <= 2 ? 4 : 2)
+norm_rope_kernel(const __grid_constant__ NormRope p) {
+  // queries: (cos, sin) of the R/2 pairs of each token, then (kStrip) a strip per
+  // warp; entries: per warp the same as doubles
   extern __shared__ double smem[];
   pdl_wait_and_release();
   const csa2_norm_rope_args& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int D = a.D;
   if ((int)blockIdx.x < p.entry_blocks) {
     const int e = blockIdx.x * p.entries_per_cta + warp;
     if (warp >= p.entries_per_cta || e >= a.E) return;
-    double* cs = smem + (size_t)warp * 2 * a.R;
+    constexpr bool kStripped = kPath == kExchange || kPath == kStrip;
+    double* cs = smem + (size_t)warp * (a.R + (kStripped ? strip_at(D) : 0));
     const int pos = __ldg(a.kv_pos + e);
     if (lane == 0 && pos < 0) record_error(p.err, CSA2_ERR_DEVICE_INDEX);
     for (int i = lane; i < a.R / 2; i += 32) {
@@ -326,15 +360,21 @@ __global__ void __launch_bounds__(kThreads, J <= 2 ? 4 : 2) norm_rope_kernel(con
       cs[2 * i + 1] = (a.inverse ? -s : s) * (double)a.rot_scale;
     }
     __syncwarp();
-    entry_row<J>(p, e, cs + a.R, cs);
+    entry_row<J, kPath>(p, e, cs + a.R, cs);
     return;
   }
   const int blk = blockIdx.x - p.entry_blocks;
-  const int t = blk / p.q_blocks, h0 = (blk % p.q_blocks) * p.heads_per_cta;
-  const int h1 = min(a.Hq, h0 + p.heads_per_cta);
-  float* cs = reinterpret_cast<float*>(smem);
-  float* strip = cs + a.R + warp * a.R;
-  const int D = a.D;
+  const bool packed = p.q_blocks == 0;
+  const int t0 = packed ? blk * p.tokens_per_cta : blk / p.q_blocks;
+  const int tokens = packed ? min(p.tokens_per_cta, a.T - t0) : 1;
+  const int tok = packed ? warp / a.Hq : 0;            // this warp's token, from t0 on
+  const int t = min(t0 + tok, a.T - 1);
+  const int h0 = packed ? warp - tok * a.Hq : (blk % p.q_blocks) * p.heads_per_cta + warp;
+  const int h1 = packed ? (tok < tokens ? h0 + 1 : h0)
+                        : min(a.Hq, (blk % p.q_blocks + 1) * p.heads_per_cta);
+  float* table = reinterpret_cast<float*>(smem);
+  const float* cs = table + tok * a.R;
+  float* strip = table + (size_t)p.tokens_per_cta * a.R + (size_t)warp * strip_at(D);
   constexpr int kRows = kWide ? 1 : 2;                 // heads of a warp in flight
   constexpr int kVecs = kWide ? 2 : 1;                 // 16-byte words of a chunk
   uint4 raw[kRows][J][kVecs];
@@ -353,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, J <= 2 ? 4 : 2) norm_rope_kernel(con
                       : make_uint4(0, 0, 0, 0);
   };
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) load(h0 + warp + r * kWarps, raw[r]);
+  for (int r = 0; r < kRows; ++r) load(h0 + r * kWarps, raw[r]);
   uint64_t w[J][4];
   const bool weighted = a.q_norm && a.q_weight != nullptr;
 #pragma unroll
@@ -366,17 +406,18 @@ __global__ void __launch_bounds__(kThreads, J <= 2 ? 4 : 2) norm_rope_kernel(con
                                    : pack2(1.0f, 1.0f);
   }
   if (kPath != kNone) {
-    const int pos = __ldg(a.pos + t);
-    if (threadIdx.x == 0 && pos < 0) record_error(p.err, CSA2_ERR_DEVICE_INDEX);
-    for (int i = threadIdx.x; i < a.R / 2; i += kThreads) {
+    for (int i = threadIdx.x; i < tokens * (a.R / 2); i += kThreads) {
+      const int k = i / (a.R / 2), pair = i - k * (a.R / 2);
+      const int pos = __ldg(a.pos + t0 + k);
+      if (pair == 0 && pos < 0) record_error(p.err, CSA2_ERR_DEVICE_INDEX);
       float s, c;
-      sincospif((float)turn_fraction(pos, a.turns[i]) * 0x1p-63f, &s, &c);
-      cs[2 * i] = c * a.rot_scale;
-      cs[2 * i + 1] = (a.inverse ? -s : s) * a.rot_scale;
+      sincospif((float)turn_fraction(pos, a.turns[pair]) * 0x1p-63f, &s, &c);
+      table[2 * i] = c * a.rot_scale;
+      table[2 * i + 1] = (a.inverse ? -s : s) * a.rot_scale;
     }
     __syncthreads();
   }
-  for (int h = h0 + warp; h < h1; h += kRows * kWarps) {
+  for (int h = h0; h < h1; h += kRows * kWarps) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int hr = h + r * kWarps;
@@ -437,6 +478,7 @@ cudaError_t launch_j(int path, const NormRope& p, unsigned grid, size_t smem,
                      cudaStream_t stream) {
   void (*kernel)(const NormRope) = path == kNone     ? norm_rope_kernel<J, kNone, kWide>
                                    : path == kInLane ? norm_rope_kernel<J, kInLane, kWide>
+                                   : path == kPairs ? norm_rope_kernel<J, kPairs, kWide>
                                    : path == kExchange ? norm_rope_kernel<J, kExchange, kWide>
                                                        : norm_rope_kernel<J, kStrip, kWide>;
   return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, dim3(1), p);
@@ -472,24 +514,38 @@ cudaError_t launch_qk_norm_rope(const csa2_norm_rope_args& a, const fp4_kv_pages
   while (p.heads_per_cta < 8 * kWarps && p.heads_per_cta < a.Hq &&
          (long long)a.T * ceil_div(a.Hq, 2 * p.heads_per_cta) >= 8ll * sms)
     p.heads_per_cta *= 2;
-  p.q_blocks = a.T > 0 ? ceil_div(a.Hq, p.heads_per_cta) : 0;
-  // entries: as many warps as 48 KB of strips allow (R = 1024: three)
-  const size_t per_entry = 2 * (size_t)a.R * sizeof(double);
+  p.q_blocks = ceil_div(a.T > 0 ? a.Hq : 1, p.heads_per_cta);
+  int path = kStrip;
+  if (a.R == 0) path = kNone;
+  else if (a.interleaved && a.rot_begin % 2 == 0)
+    path = a.rot_begin % 8 == 0 && a.R % 8 == 0 ? kInLane : kPairs;
+  else if (!a.interleaved && a.R % 16 == 0 && a.rot_begin % 8 == 0 &&
+           a.rot_begin / 256 == (a.rot_begin + a.R - 1) / 256)
+    path = kExchange;
+  p.tokens_per_cta = 1;
+  long long query_blocks = (long long)a.T * p.q_blocks;
+  if (a.T > 1 && a.Hq <= kWarps / 2) {
+    // few heads: whole tokens share a CTA, while their tables and strips stay in 48 KB
+    // (3228 tokens of one head of 128 and 911 entries: 10 us, a CTA per token 16-18)
+    const int tables = (48 * 1024 / 4 - (path == kStrip ? kWarps * strip_at(a.D) : 0)) /
+                       (a.R > 0 ? a.R : 1);
+    p.q_blocks = 0;
+    p.tokens_per_cta = kWarps / a.Hq < tables ? kWarps / a.Hq : tables;
+    query_blocks = ceil_div(a.T, p.tokens_per_cta);
+  }
+  // entries: as many warps as 48 KB of tables and strips allow (D = R = 1024: three)
+  const size_t per_entry =
+      (a.R + (path == kExchange || path == kStrip ? strip_at(a.D) : 0)) * sizeof(double);
   p.entries_per_cta = per_entry * kWarps <= 48 * 1024 ? kWarps : (int)(48 * 1024 / per_entry);
   // few entries: a CTA each, as their chains are what a small call waits for
   if (a.E <= sms) p.entries_per_cta = 1;
   p.entry_blocks = ceil_div(a.E, p.entries_per_cta);
-  const long long grid = (long long)p.entry_blocks + (long long)a.T * p.q_blocks;
+  const long long grid = (long long)p.entry_blocks + query_blocks;
   if (grid == 0) return cudaSuccess;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-  int path = kStrip;
-  if (a.R == 0) path = kNone;
-  else if (a.interleaved && a.rot_begin % 8 == 0 && a.R % 8 == 0) path = kInLane;
-  else if (!a.interleaved && a.R % 16 == 0 && a.rot_begin % 8 == 0 &&
-           a.rot_begin / 256 == (a.rot_begin + a.R - 1) / 256)
-    path = kExchange;
   const size_t for_entries = a.E > 0 ? p.entries_per_cta * per_entry : 0;
-  const size_t for_queries = (path == kStrip ? 1 + kWarps : 1) * (size_t)a.R * sizeof(float);
+  const size_t for_queries = ((size_t)p.tokens_per_cta * a.R +
+                              (path == kStrip ? (size_t)kWarps * strip_at(a.D) : 0)) * sizeof(float);
   const size_t smem = for_entries > for_queries ? for_entries : for_queries;
   return a.T > 0 && a.q_f32 ? launch_wide<true>(path, p, (unsigned)grid, smem, stream)
                             : launch_wide<false>(path, p, (unsigned)grid, smem, stream);

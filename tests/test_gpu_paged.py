@@ -244,12 +244,20 @@ def bf16(x):
     (1024, 4, 5, 5, 1024, 0, True, True, True, True, False),
     (768, 2, 3, 1, 0, 0, True, False, True, True, False),
     (256, 40, 200, 0, 128, 128, False, False, True, False, False),
-    (512, 1, 0, 6, 64, 448, True, False, True, True, False)])
+    (512, 1, 0, 6, 64, 448, True, False, True, True, False),
+    # few heads: several tokens share a CTA, the last one fewer
+    (1024, 1, 9, 6, 1024, 0, False, False, True, True, False),
+    (512, 1, 19, 9, 78, 434, False, False, True, True, False),
+    (512, 4, 7, 2, 184, 52, True, True, True, False, True),
+    (128, 3, 5, 5, 70, 2, True, False, True, True, False),
+    (256, 2, 9, 300, 64, 61, True, False, True, True, False),
+    (384, 8, 9, 160, 64, 316, False, True, True, True, False),
+    (512, 64, 5, 3, 70, 442, False, False, True, True, False)])
 def test_norm_rope_append(D, H, T, E, R, begin, inter, wide, norm, weight, inverse):
     r = np.random.RandomState(D + H + T)
-    S, page, M = 3, 16, 4
+    S, page, M = 3, 16, 4 if E <= 84 else 8
     m, g = caches(S * M + 2, page, D, S, M, seed=3)
-    resize(m, g, range(S), [40, 64, 33])
+    resize(m, g, range(S), [40, 64, 33] if M == 4 else [105, 128, 110])
     # queries and entries are slices of one projection
     n = max(T, E, 1)
     x = (r.standard_normal((n, (H + 1) * D + 8)) * 2).astype(np.float32)
