@@ -17,9 +17,10 @@
 // batch keeps every SM busy. (Before each pair's tiles the line has kSetup units of
 // nothing, what a further pair costs a piece: its query block and its output take
 // as long as four tiles. Without them, pieces with two pairs ended 10 us after
-// the others, of 24 us.) A pair that lies within one piece is written out;
-// one that is cut leaves fp16 partials with their (maximum, sum), which
-// paged_combine_kernel joins. A sequence without entries has one empty tile.
+// the others, of 24 us.) Where the pairs are short, the pieces are whole pairs. A
+// pair that lies within one piece is written out; one that is cut leaves fp16
+// partials with their (maximum, sum), which paged_combine_kernel joins. A sequence
+// without entries has one empty tile.
 //
 // With lists each query token is a sequence of its own here, its list the entries
 // (a place without an id takes its turn as an entry that is not there).
@@ -121,7 +122,10 @@ struct __align__(16) Smem {
   int abort_flag;
   long long total;                  // units of the line
   long long pos, end;               // this piece's units not yet in a segment
+  long long end_pair;               // pairs from this one on are not this piece's
   long long base;                   // units before the sequence that pos lies in
+  int most[kThreads / 32];          // units of the longest pair, by warp
+  int whole;                        // pairs are dealt out whole
   uint4 valid[4];                   // bit i of a tile's 128: entry i is there
   float2 mlf[kRows];                // (reference maximum, row sum)
   float qdown[kRows];               // the power of two each row was scaled up by, inverted
@@ -134,6 +138,7 @@ struct Params {
   const uint16_t* q;
   fp4_kv_pages pg;
   int shift;
+  long long share;     // pairs that a piece has at most if they are dealt out whole
   const int32_t* seq;
   const int32_t* nvalid;
   const int32_t* ids;  // [B][K], or null for every entry
@@ -397,10 +402,16 @@ __device__ __noinline__ void next_segment(const Params& p, Smem& sm, int at, int
   s.nt = 0;
   s.blk = s.t0 = s.n_most = s.tiles = s.slot = 0;
   long long pos = sm.pos;
+  const long long last_pair = sm.end_pair - 1;
   if (pos < sm.end) {
     if (prev.nt > 0 && pos == sm.base + (long long)p.nblk * (kSetup + prev.tiles)) {
       sm.base = pos;
       ++s.b;
+    }
+    if ((long long)s.b * p.nblk > last_pair) {           // whole pairs, and they are done
+      sm.pos = sm.end;
+      sm.seg[at] = s;
+      return;
     }
     const int pieces = (int)min((long long)gridDim.x, sm.total), piece = (int)blockIdx.x;
     s.n_most = n_most >= 0 ? n_most : entries_of<kListed>(p, s.b, false);
@@ -410,13 +421,15 @@ __device__ __noinline__ void next_segment(const Params& p, Smem& sm, int at, int
     const long long first = sm.base + (long long)s.blk * units + kSetup;   // the pair's first tile
     pos = max(pos, first);
     s.t0 = (int)(pos - first);
-    s.nt = (int)max(0ll, min((long long)(s.tiles - s.t0), sm.end - pos));
+    s.nt = (long long)s.b * p.nblk + s.blk > last_pair
+               ? 0 : (int)max(0ll, min((long long)(s.tiles - s.t0), sm.end - pos));
     if (s.nt > 0) {
       const int slot = 2 * piece + (prev.nt > 0 ? 1 : 0);
       s.slot = s.nt == s.tiles ? -1 : slot;
       if (s.t0 == 0)
         p.ws_info[(size_t)s.b * p.nblk + s.blk] =
-            make_int4(piece, piece_of(first + s.tiles - 1, pieces, sm.total), slot, 0);
+            make_int4(piece, s.nt == s.tiles ? piece : piece_of(first + s.tiles - 1, pieces, sm.total),
+                      slot, 0);
     }
     sm.pos = s.nt > 0 ? pos + s.nt : sm.end;
   }
@@ -455,12 +468,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
     const int each = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, (int)threadIdx.x * each), b1 = min(p.B, b0 + each);
     long long mine = 0;
-    int n_last = 0;
+    int n_last = 0, most = 0;                            // units of the longest pair
     for (int b = b0; b < b1; ++b) {
       n_last = entries_of<kListed>(p, b, blockIdx.x == 0);
       mine += (long long)p.nblk * pair_units(n_last);
+      most = max(most, pair_units(n_last));
     }
     sums[threadIdx.x] = mine;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) sm.most[warp] = most;
     __syncthreads();
     if (threadIdx.x < 32) {
       long long run = 0;
@@ -475,28 +491,57 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
         sums[i] = run + incl - x;
         run += __shfl_sync(0xffffffffu, incl, 31);
       }
-      if (lane == 0) sm.total = run;
+      // Short pairs are better dealt out whole than cut: the longest such share against
+      // an even piece, one of whose pairs is cut (its query block is read again).
+      // 36 sequences of 3 to 169 entries with 256 rows: 21 us whole, 28 cut.
+      most = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? sm.most[lane] : 0);
+      if (lane == 0) {
+        sm.total = run;
+        const long long pieces = min((long long)gridDim.x, run);
+        sm.whole = p.share * most * pieces <= run + kSetup * pieces;
+      }
     }
     __syncthreads();
     const long long total = sm.total;
     const int pieces = (int)min((long long)gridDim.x, total);
     const long long before = sums[threadIdx.x];
-    const long long begin = piece_begin(min((int)blockIdx.x, pieces - 1), pieces, total);
-    if (begin >= before && begin < before + mine) {
-      long long at = before;
-      int b = b0;
-      for (; b + 1 < b1; ++b) {
-        const long long k = (long long)p.nblk * pair_units(entries_of<kListed>(p, b, false));
-        if (begin < at + k) break;
-        at += k;
+    const long long pairs = (long long)p.B * p.nblk;
+    if (sm.whole) {
+      const long long j0 = quotient(blockIdx.x * pairs, gridDim.x);
+      const int b = (int)quotient(j0, p.nblk);
+      if (b >= b0 && b < b1) {
+        long long at = before;
+        for (int k = b0; k < b; ++k)
+          at += (long long)p.nblk * pair_units(entries_of<kListed>(p, k, false));
+        const int n = each == 1 ? n_last : entries_of<kListed>(p, b, false);
+        sm.seg[1].b = b;
+        sm.base = at;
+        sm.seg[1].nt = 0;
+        sm.seg[1].g0 = sm.seg[1].used0 = sm.seg[1].used1 = 0;
+        sm.pos = at + (j0 - (long long)b * p.nblk) * pair_units(n);
+        sm.end = total;
+        sm.end_pair = quotient((blockIdx.x + 1) * pairs, gridDim.x);
+        next_segment<kListed>(p, sm, 0, n);
       }
-      sm.seg[1].b = b;
-      sm.base = at;
-      sm.seg[1].nt = 0;
-      sm.seg[1].g0 = sm.seg[1].used0 = sm.seg[1].used1 = 0;
-      sm.pos = begin;
-      sm.end = (int)blockIdx.x < pieces ? piece_begin((int)blockIdx.x + 1, pieces, total) : begin;
-      next_segment<kListed>(p, sm, 0, each == 1 ? n_last : -1);
+    } else {
+      const long long begin = piece_begin(min((int)blockIdx.x, pieces - 1), pieces, total);
+      if (begin >= before && begin < before + mine) {
+        long long at = before;
+        int b = b0;
+        for (; b + 1 < b1; ++b) {
+          const long long k = (long long)p.nblk * pair_units(entries_of<kListed>(p, b, false));
+          if (begin < at + k) break;
+          at += k;
+        }
+        sm.seg[1].b = b;
+        sm.base = at;
+        sm.seg[1].nt = 0;
+        sm.seg[1].g0 = sm.seg[1].used0 = sm.seg[1].used1 = 0;
+        sm.pos = begin;
+        sm.end_pair = pairs;
+        sm.end = (int)blockIdx.x < pieces ? piece_begin((int)blockIdx.x + 1, pieces, total) : begin;
+        next_segment<kListed>(p, sm, 0, each == 1 ? n_last : -1);
+      }
     }
   }
   tc_fence_before();
@@ -1080,67 +1125,106 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
   if (threadIdx.x == 0 && *abort_flag) record_error(p.err, CSA2_ERR_TIMEOUT);
 }
 
-// Joins the pieces of one query row: out = sum_i w_i o_i / sum_i w_i, w_i = 2^(m_i - M) l_i.
-// 64 threads hold a row's 512 channels (one 16-byte load per piece). kGroups = 1:
-// four rows per CTA; 4: one row, its pieces shared out over four groups. Rows are
-// many when each comes from few pieces (2280 rows of 4 to 9: four rows per CTA 5 us
-// less than one), and few when they come from many (256 rows of 37: one per CTA).
-template <int kGroups>
+// Joins the pieces of one query row: out = sum_i w_i o_i / sum_i w_i, w_i = 2^(m_i - M) l_i,
+// in one pass with the running M. A thread holds 8 channels (a 16-byte load per piece),
+// kLanes threads 8 kLanes of the 512, and kGroups such groups share out the pieces,
+// four pieces of each on their way at a time. Bound: the latency of those loads, so
+// few rows, which come from many pieces, take many groups and CTAs. Measured (whole call):
+// 64 rows of 148 pieces, 16 groups on 4 CTAs: 38 us of the call's, 4 groups on one 45;
+// 512 rows of 19, 4 groups: 41 us, 16 groups 45; 960 rows of 10, one group: 30 us (16: 37).
+template <int kLanes, int kGroups>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const Params p, int b0) {
-  constexpr int kRowsPerCta = 4 / kGroups;
-  __shared__ float part[kGroups][64][9];               // (kGroups > 1) 8 channels, weight
+  constexpr int kRowsPerCta = 256 / (kLanes * kGroups), kParts = 64 / kLanes;
+  constexpr int kBatch = 4, kChannels = 8 * kLanes;
+  static_assert(kGroups == 1 || kRowsPerCta == 1, "the groups of a row are the CTA");
+  __shared__ __align__(16) float part[kGroups][kGroups > 1 ? kChannels : 4];
+  __shared__ float2 part_ml[kGroups];
   pdl_wait_and_release();
   const int per_seq = p.Tq * p.Hq;
-  const int unit = threadIdx.x >> 6, grp = unit % kGroups;
-  const int r = blockIdx.x * kRowsPerCta + unit / kGroups;         // row of the sequence
+  const int grp = threadIdx.x / kLanes % kGroups;
+  const int r = blockIdx.x / kParts * kRowsPerCta + threadIdx.x / (kLanes * kGroups);
   if (r >= per_seq) return;
   const size_t b = (size_t)b0 + blockIdx.y;
   const int4 info = p.ws_info[b * p.nblk + r / kRows];
   const int first = info.x, last = info.y;
   if (first == last) return;
-  const int h = r % kRows, lane = threadIdx.x & 31, c = threadIdx.x & 63;
-  auto slot_of = [&](int i) { return (size_t)(i == first ? info.z : 2 * i) * kRows + h; };
-  float M = -INFINITY;
-  for (int i = first + lane; i <= last; i += 32) M = fmaxf(M, p.ws_ml[slot_of(i)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.0f;
+  const int h = r % kRows;
+  const int c = blockIdx.x % kParts * kLanes + threadIdx.x % kLanes;   // of 64, 8 channels each
+  float M = -INFINITY, L = 0.0f;
   float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  if (M != -INFINITY) {
-#pragma unroll 4
-    for (int i = first + grp; i <= last; i += kGroups) {
-      const float2 ml = p.ws_ml[slot_of(i)];
-      const uint4 u = *reinterpret_cast<const uint4*>(p.ws_o + slot_of(i) * kD + 8 * c);
-      const float w = exp2f(ml.x - M) * ml.y;          // 0 for a piece that saw nothing
-      const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+  for (int i0 = first + grp; i0 <= last; i0 += kGroups * kBatch) {
+    float2 ml[kBatch];
+    uint4 u[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kGroups;
+      ml[k] = make_float2(-INFINITY, 0.0f);
+      u[k] = make_uint4(0, 0, 0, 0);
+      if (i <= last) {
+        const size_t at = (size_t)(i == first ? info.z : 2 * i) * kRows + h;
+        ml[k] = p.ws_ml[at];
+        u[k] = *reinterpret_cast<const uint4*>(p.ws_o + at * kD + 8 * c);
+      }
+    }
+    float m = M;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) m = fmaxf(m, ml[k].x);
+    if (m == -INFINITY) continue;                      // pieces that saw nothing
+    const float f = exp2f(M - m);
+    M = m;
+    L *= f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] *= f;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float w = exp2f(ml[k].x - M) * ml[k].y;    // 0 for a piece that saw nothing
+      const uint32_t v[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
       L += w;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[k]));
-        acc[2 * k] = fmaf(w, f.x, acc[2 * k]);
-        acc[2 * k + 1] = fmaf(w, f.y, acc[2 * k + 1]);
+      for (int q = 0; q < 4; ++q) {
+        const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&v[q]));
+        acc[2 * q] = fmaf(w, o.x, acc[2 * q]);
+        acc[2 * q + 1] = fmaf(w, o.y, acc[2 * q + 1]);
       }
     }
   }
-  if (kGroups > 1) {
+  const size_t row = b * per_seq + r;
+  if (kGroups == 1) {
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    reinterpret_cast<uint4*>(p.out + row * kD)[c] =
+        make_uint4(pack_bf162(acc[0] * inv, acc[1] * inv), pack_bf162(acc[2] * inv, acc[3] * inv),
+                   pack_bf162(acc[4] * inv, acc[5] * inv), pack_bf162(acc[6] * inv, acc[7] * inv));
+    if (p.lse && c == 0) p.lse[row] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    return;
+  }
+  const int lane = threadIdx.x % kLanes;
+  *reinterpret_cast<float4*>(&part[grp][8 * lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  *reinterpret_cast<float4*>(&part[grp][8 * lane + 4]) =
+      make_float4(acc[4], acc[5], acc[6], acc[7]);
+  if (lane == 0) part_ml[grp] = make_float2(M, L);
+  __syncthreads();
+  if (threadIdx.x >= kChannels / 2) return;            // two channels each
+  M = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) part[grp][c][k] = acc[k];
-    part[grp][c][8] = L;
-    __syncthreads();                                   // (one row: the CTA is here or has left)
-    if (grp > 0) return;
+  for (int g = 0; g < kGroups; ++g) M = fmaxf(M, part_ml[g].x);
+  float2 o = make_float2(0.0f, 0.0f);
+  L = 0.0f;
+  if (M != -INFINITY) {
 #pragma unroll
-    for (int g = 1; g < kGroups; ++g) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] += part[g][c][k];
-      L += part[g][c][8];
+    for (int g = 0; g < kGroups; ++g) {
+      const float2 ml = part_ml[g];
+      const float f = exp2f(ml.x - M);
+      const float2 v = *reinterpret_cast<const float2*>(&part[g][2 * threadIdx.x]);
+      L = fmaf(f, ml.y, L);
+      o.x = fmaf(f, v.x, o.x);
+      o.y = fmaf(f, v.y, o.y);
     }
   }
   const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-  const size_t row = b * per_seq + r;
-  reinterpret_cast<uint4*>(p.out + row * kD)[c] =
-      make_uint4(pack_bf162(acc[0] * inv, acc[1] * inv), pack_bf162(acc[2] * inv, acc[3] * inv),
-                 pack_bf162(acc[4] * inv, acc[5] * inv), pack_bf162(acc[6] * inv, acc[7] * inv));
-  if (p.lse && c == 0) p.lse[row] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  reinterpret_cast<uint32_t*>(p.out + row * kD)[blockIdx.x % kParts * (kChannels / 2) + threadIdx.x] =
+      pack_bf162(o.x * inv, o.y * inv);
+  if (p.lse && blockIdx.x % kParts == 0 && threadIdx.x == 0)
+    p.lse[row] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
 int sm_count_of_device() {
@@ -1220,6 +1304,7 @@ cudaError_t launch_paged_attn(const uint16_t* q, const fp4_kv_pages& pg, const i
   p.out = out;
   p.lse = lse;
   const int pieces = sh.pieces();
+  p.share = ((long long)sh.B * sh.nblk + pieces - 1) / pieces;
   unsigned char* w = static_cast<unsigned char*>(workspace);
   p.ws_info = reinterpret_cast<int4*>(w);
   w += up256((size_t)sh.B * sh.nblk * sizeof(int4));
@@ -1236,10 +1321,16 @@ cudaError_t launch_paged_attn(const uint16_t* q, const fp4_kv_pages& pg, const i
   const int rows = sh.rows;
   for (int b0 = 0; b0 < sh.B; b0 += 65535) {
     const unsigned nb = (unsigned)(sh.B - b0 < 65535 ? sh.B - b0 : 65535);
-    if ((long long)sh.B * rows <= 8 * sm_count_of_device())
-      e = launch_pdl(paged_combine_kernel<4>, dim3(rows, nb), dim3(256), 0, stream, dim3(1), p, b0);
+    const long long all = (long long)sh.B * rows;
+    const int sms = sm_count_of_device();
+    if (all <= 2 * sms)
+      e = launch_pdl(paged_combine_kernel<16, 16>, dim3(4 * rows, nb), dim3(256), 0, stream, dim3(1),
+                     p, b0);
+    else if (all <= 8 * sms)
+      e = launch_pdl(paged_combine_kernel<64, 4>, dim3(rows, nb), dim3(256), 0, stream, dim3(1), p,
+                     b0);
     else
-      e = launch_pdl(paged_combine_kernel<1>, dim3(ceil_div(rows, 4), nb), dim3(256), 0, stream,
+      e = launch_pdl(paged_combine_kernel<64, 1>, dim3(ceil_div(rows, 4), nb), dim3(256), 0, stream,
                      dim3(1), p, b0);
     if (e != cudaSuccess) return e;
   }

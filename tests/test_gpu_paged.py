@@ -414,7 +414,12 @@ def check_attn(m, slots, q, got, lse, scale, nvalid=None, ids=None):
     (1, 1, 64, [97], 64), (2, 1, 64, [0, 193], 8), (3, 2, 24, [1, 2, 500], 32),
     (2, 3, 40, [0, 777], 16), (1, 1, 128, [640], 128), (5, 1, 8, [64, 128, 192, 63, 65], 64),
     (1, 4, 64, [2049], 256), (1, 1, 64, [20000], 64), (40, 1, 64, [300 + 7 * i for i in range(40)], 16),
-    (3, 1, 200, [130, 0, 5], 8)])
+    (3, 1, 200, [130, 0, 5], 8),
+    # short pairs, dealt out whole: one, two and four to an SM of 148; and one that is long
+    (36, 2, 70, [(37 * i) % 161 for i in range(36)], 16),
+    (98, 3, 64, [81 + (i * 7) % 80 for i in range(98)], 32),
+    (590, 1, 8, [(i * 11) % 81 for i in range(590)], 8),
+    (36, 2, 70, [(37 * i) % 161 + 2000 * (i == 20) for i in range(36)], 16)])
 def test_dense(B, Tq, H, lens, page):
     m, g, slots, q = attn_case(B, Tq, H, lens, page)
     scale = 1 / math.sqrt(512)
