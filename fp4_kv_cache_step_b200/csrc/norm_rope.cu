@@ -20,8 +20,8 @@
 // An entry's group of 16 channels is two neighbouring lanes: one exchange gives its
 // maximum, the codes of a lane are one 32-bit word. Bound: HBM (a few dozen
 // instructions per 16 bytes read and written); at single tokens, the launch. Measured:
-// 4096 tokens of 64 heads of 512 channels (bf16) and 1024 entries, 539 MB, in 94 to
-// 98 us, 5.5 to 5.7 TB/s (a plain copy: 6.5).
+// 4096 tokens of 64 heads of 512 channels (bf16) and 1024 entries, 539 MB, in 90 us,
+// 6.0 TB/s (a plain copy: 6.5).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -334,9 +334,15 @@ __device__ __forceinline__ void rotate_row(const csa2_norm_rope_args& a, uint64_
 // CTAs [0, entry_blocks) take entries, one per warp (they come first, being the
 // longest chains); the others heads_per_cta heads of a token, or all heads of
 // tokens_per_cta tokens, a row per warp.
-// (64 registers a thread where they suffice: 32 warps per SM, 2 KB each in flight)
+// 64 registers a thread where they nearly suffice: 32 warps per SM, 2 KB each in flight.
+// Elsewhere 80 and 24 warps (2000 tokens of 40 heads of 512 rotated in halves: 37 us, 42
+// with 64 registers; neighbouring channels in whole chunks 34 and 33).
+constexpr int min_ctas(int J, int path, bool wide) {
+  const bool light = path == kNone || path == kInLane || (path == kPairs && wide);
+  return J > 2 ? 2 : light ? 4 : 3;
+}
 template <int J, int kPath, bool kWide>
-__global__ void __launch_bounds__(kThreads, J <= 2 ? 4 : 2)
+__global__ void __launch_bounds__(kThreads, min_ctas(J, kPath, kWide))
 norm_rope_kernel(const __grid_constant__ NormRope p) {
   // queries: (cos, sin) of the R/2 pairs of each token, then (kStrip) a strip per
   // warp; entries: per warp the same as doubles
