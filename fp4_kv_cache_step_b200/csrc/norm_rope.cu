@@ -20,8 +20,8 @@
 // An entry's group of 16 channels is two neighbouring lanes: one exchange gives its
 // maximum, the codes of a lane are one 32-bit word. Bound: HBM (a few dozen
 // instructions per 16 bytes read and written); at single tokens, the launch. Measured:
-// 4096 tokens of 64 heads of 512 channels (bf16) and 1024 entries, 539 MB, in 90 us,
-// 6.0 TB/s (a plain copy: 6.5).
+// 4096 tokens of 64 heads of 512 channels (bf16) and 1024 entries, 539 MB, in 88 us,
+// 6.1 TB/s (a plain copy: 6.5).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -61,9 +61,9 @@ struct NormRope {
   fp4_kv_pages pg;
   int shift;
   int entry_blocks, entries_per_cta;
-  int q_blocks;      // CTAs per token's heads, or 0: tokens_per_cta tokens of few heads
+  int rows_per_cta;  // (token, head) rows, of tokens_per_cta tokens at most
   int tokens_per_cta;
-  int heads_per_cta;
+  int step_tok, step_head;   // kWarps rows as tokens and heads
   int* err;
 };
 
@@ -332,24 +332,20 @@ __device__ __forceinline__ void rotate_row(const csa2_norm_rope_args& a, uint64_
 }
 
 // CTAs [0, entry_blocks) take entries, one per warp (they come first, being the
-// longest chains); the others heads_per_cta heads of a token, or all heads of
-// tokens_per_cta tokens, a row per warp.
-// 64 registers a thread where they nearly suffice: 32 warps per SM, 2 KB each in flight.
-// Elsewhere 80 and 24 warps (2000 tokens of 40 heads of 512 rotated in halves: 37 us, 42
-// with 64 registers; neighbouring channels in whole chunks 34 and 33).
-constexpr int min_ctas(int J, int path, bool wide) {
-  const bool light = path == kNone || path == kInLane || (path == kPairs && wide);
-  return J > 2 ? 2 : light ? 4 : 3;
-}
+// longest chains); the others rows_per_cta (token, head) rows, warp w every 8th from w.
+// 64 registers a thread where they suffice: 32 warps per SM, 2 KB each in flight.
+// Elsewhere 80 and 24 warps (2000 tokens of 40 heads of 512 rotated in halves: 36 us,
+// with 64 registers 42; neighbouring channels in whole chunks 32 and 33).
+constexpr int min_ctas(int J, int path) { return J > 2 ? 2 : path <= kInLane ? 4 : 3; }
 template <int J, int kPath, bool kWide>
-__global__ void __launch_bounds__(kThreads, min_ctas(J, kPath, kWide))
+__global__ void __launch_bounds__(kThreads, min_ctas(J, kPath))
 norm_rope_kernel(const __grid_constant__ NormRope p) {
   // queries: (cos, sin) of the R/2 pairs of each token, then (kStrip) a strip per
   // warp; entries: per warp the same as doubles
   extern __shared__ double smem[];
   pdl_wait_and_release();
   const csa2_norm_rope_args& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int D = a.D;
   if ((int)blockIdx.x < p.entry_blocks) {
     const int e = blockIdx.x * p.entries_per_cta + warp;
@@ -369,37 +365,46 @@ norm_rope_kernel(const __grid_constant__ NormRope p) {
     entry_row<J, kPath>(p, e, cs + a.R, cs);
     return;
   }
-  const int blk = blockIdx.x - p.entry_blocks;
-  const bool packed = p.q_blocks == 0;
-  const int t0 = packed ? blk * p.tokens_per_cta : blk / p.q_blocks;
-  const int tokens = packed ? min(p.tokens_per_cta, a.T - t0) : 1;
-  const int tok = packed ? warp / a.Hq : 0;            // this warp's token, from t0 on
-  const int t = min(t0 + tok, a.T - 1);
-  const int h0 = packed ? warp - tok * a.Hq : (blk % p.q_blocks) * p.heads_per_cta + warp;
-  const int h1 = packed ? (tok < tokens ? h0 + 1 : h0)
-                        : min(a.Hq, (blk % p.q_blocks + 1) * p.heads_per_cta);
+  const int Hq = a.Hq;
+  const long long r0 = (long long)(blockIdx.x - p.entry_blocks) * p.rows_per_cta;
+  const int rows = (int)min((long long)p.rows_per_cta, (long long)a.T * Hq - r0);
+  const int t0 = (int)(r0 / Hq), h0 = (int)(r0 - (long long)t0 * Hq);    // the first row's
+  const int tokens = (h0 + rows - 1) / Hq + 1;
   float* table = reinterpret_cast<float*>(smem);
-  const float* cs = table + tok * a.R;
   float* strip = table + (size_t)p.tokens_per_cta * a.R + (size_t)warp * strip_at(D);
-  constexpr int kRows = kWide ? 1 : 2;                 // heads of a warp in flight
+  constexpr int kRows = kWide ? 1 : J == 1 ? 4 : 2;    // rows of a warp in flight
   constexpr int kVecs = kWide ? 2 : 1;                 // 16-byte words of a chunk
   uint4 raw[kRows][J][kVecs];
   const float inv_d = 1.0f / D;
   const int esz = kWide ? 4 : 2;
-  const char* src = static_cast<const char*>(a.q) + ((size_t)t * a.q_stride + lane * 8) * esz;
-  uint16_t* dst = a.q_out + (size_t)t * a.Hq * D + lane * 8;
-  auto load = [&](int h, uint4 (&v)[J][kVecs]) {
+  const size_t token_bytes = (size_t)a.q_stride * esz;
+  const char* src = static_cast<const char*>(a.q) + (size_t)t0 * token_bytes + lane * 8 * esz;
+  uint16_t* dst = a.q_out + r0 * D + lane * 8;
+  // (token, head) of this warp's next row to load and to compute, kWarps rows apart
+  int load_row = warp, load_tok = (h0 + warp) / Hq, load_h = h0 + warp - load_tok * Hq;
+  int tok = load_tok, head = load_h;
+  auto next = [&](int& t, int& h) {
+    t += p.step_tok;
+    h += p.step_head;
+    if (h >= Hq) {
+      h -= Hq;
+      ++t;
+    }
+  };
+  auto load = [&](uint4 (&v)[J][kVecs]) {
+    const char* at = src + (size_t)load_tok * token_bytes + (size_t)(load_h * D * esz);
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int k = 0; k < kVecs; ++k)
-        v[j][k] = h < h1 && (lane + 32 * j) * 8 < D
-                      ? __ldcs(reinterpret_cast<const uint4*>(
-                            src + ((size_t)h * D + 256 * j + 4 * k) * esz))
+        v[j][k] = load_row < rows && (lane + 32 * j) * 8 < D
+                      ? __ldcs(reinterpret_cast<const uint4*>(at + (256 * j + 4 * k) * esz))
                       : make_uint4(0, 0, 0, 0);
+    load_row += kWarps;
+    next(load_tok, load_h);
   };
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) load(h0 + r * kWarps, raw[r]);
+  for (int r = 0; r < kRows; ++r) load(raw[r]);
   uint64_t w[J][4];
   const bool weighted = a.q_norm && a.q_weight != nullptr;
 #pragma unroll
@@ -423,11 +428,10 @@ norm_rope_kernel(const __grid_constant__ NormRope p) {
     }
     __syncthreads();
   }
-  for (int h = h0; h < h1; h += kRows * kWarps) {
+  for (int row = warp; row < rows;) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int hr = h + r * kWarps;
-      if (hr >= h1) break;                             // the same for every lane
+      if (row >= rows) break;                          // the same for every lane
       uint64_t y[J][4];
 #pragma unroll
       for (int j = 0; j < J; ++j) {
@@ -446,7 +450,7 @@ norm_rope_kernel(const __grid_constant__ NormRope p) {
             y[j][k] = pack2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u));
         }
       }
-      load(hr + kRows * kWarps, raw[r]);
+      load(raw[r]);
       if (a.q_norm) {
         uint64_t s2 = 0;
 #pragma unroll
@@ -462,7 +466,7 @@ norm_rope_kernel(const __grid_constant__ NormRope p) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) y[j][k] = mul2(mul2(y[j][k], f2), w[j][k]);
       }
-      rotate_row<J, kPath>(a, y, strip, cs);
+      rotate_row<J, kPath>(a, y, strip, table + tok * a.R);
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         if ((lane + 32 * j) * 8 >= D) continue;
@@ -472,9 +476,11 @@ norm_rope_kernel(const __grid_constant__ NormRope p) {
           const float2 v = unpack2(y[j][k]);
           o[k] = pack_bf162(v.x, v.y);
         }
-        __stcs(reinterpret_cast<uint4*>(dst + (size_t)hr * D + 256 * j),
+        __stcs(reinterpret_cast<uint4*>(dst + (size_t)row * D + 256 * j),
                make_uint4(o[0], o[1], o[2], o[3]));
       }
+      row += kWarps;
+      next(tok, head);
     }
   }
 }
@@ -514,13 +520,6 @@ cudaError_t launch_qk_norm_rope(const csa2_norm_rope_args& a, const fp4_kv_pages
   int sms = 148, dev = 0;
   if (cudaGetDevice(&dev) == cudaSuccess)
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  // heads of a token per CTA: few tokens spread over the SMs a warp per head; many
-  // tokens share the cosines of a token among up to 64 of its heads
-  p.heads_per_cta = kWarps;
-  while (p.heads_per_cta < 8 * kWarps && p.heads_per_cta < a.Hq &&
-         (long long)a.T * ceil_div(a.Hq, 2 * p.heads_per_cta) >= 8ll * sms)
-    p.heads_per_cta *= 2;
-  p.q_blocks = ceil_div(a.T > 0 ? a.Hq : 1, p.heads_per_cta);
   int path = kStrip;
   if (a.R == 0) path = kNone;
   else if (a.interleaved && a.rot_begin % 2 == 0)
@@ -528,17 +527,23 @@ cudaError_t launch_qk_norm_rope(const csa2_norm_rope_args& a, const fp4_kv_pages
   else if (!a.interleaved && a.R % 16 == 0 && a.rot_begin % 8 == 0 &&
            a.rot_begin / 256 == (a.rot_begin + a.R - 1) / 256)
     path = kExchange;
-  p.tokens_per_cta = 1;
-  long long query_blocks = (long long)a.T * p.q_blocks;
-  if (a.T > 1 && a.Hq <= kWarps / 2) {
-    // few heads: whole tokens share a CTA, while their tables and strips stay in 48 KB
-    // (3228 tokens of one head of 128 and 911 entries: 10 us, a CTA per token 16-18)
-    const int tables = (48 * 1024 / 4 - (path == kStrip ? kWarps * strip_at(a.D) : 0)) /
-                       (a.R > 0 ? a.R : 1);
-    p.q_blocks = 0;
-    p.tokens_per_cta = kWarps / a.Hq < tables ? kWarps / a.Hq : tables;
-    query_blocks = ceil_div(a.T, p.tokens_per_cta);
-  }
+  // rows per CTA: few rows spread over the SMs, one per warp; many share the start and
+  // the cosines, up to 64 of them (64 KB of bf16) while the tables and strips stay in 48 KB
+  const long long all = (long long)a.T * a.Hq;
+  const long long words = 48 * 1024 / 4 - (path == kStrip ? kWarps * strip_at(a.D) : 0);
+  auto tokens_of = [&](int rows) { return a.T > 0 ? (rows - 2 + a.Hq) / a.Hq + 1 : 0; };   // touched at most
+  p.rows_per_cta = kWarps;
+  while (p.rows_per_cta > 1 && (long long)tokens_of(p.rows_per_cta) * a.R > words)
+    p.rows_per_cta /= 2;
+  const int top = a.D >= 512 || a.q_f32 ? 64 : 64 * 512 / a.D;
+  while (p.rows_per_cta < top && all / (2 * p.rows_per_cta) >= 8ll * sms &&
+         (long long)tokens_of(2 * p.rows_per_cta) * a.R <= words)
+    p.rows_per_cta *= 2;
+  p.tokens_per_cta = tokens_of(p.rows_per_cta);
+  if (p.tokens_per_cta > a.T) p.tokens_per_cta = a.T;
+  p.step_tok = a.T > 0 ? kWarps / a.Hq : 0;
+  p.step_head = a.T > 0 ? kWarps % a.Hq : 0;
+  const long long query_blocks = (all + p.rows_per_cta - 1) / p.rows_per_cta;
   // entries: as many warps as 48 KB of tables and strips allow (D = R = 1024: three)
   const size_t per_entry =
       (a.R + (path == kExchange || path == kStrip ? strip_at(a.D) : 0)) * sizeof(double);
