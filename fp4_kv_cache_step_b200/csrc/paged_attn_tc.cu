@@ -326,6 +326,21 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) {
   asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// ((a - m) s, (b - m) s), two values to an instruction
+__device__ __forceinline__ float2 scaled_difference(float a, float b, float m, float s) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %4};\n\t"
+      "add.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 y, {%5, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a), "f"(b), "f"(-m), "f"(s));
+  return r;
+}
+
 // ---------------------------------------------------------------- lengths, pieces
 __device__ __forceinline__ int slot_of(const Params& p, int b) {
   return p.seq ? __ldg(p.seq + b / p.per_slot) : b / p.per_slot;
@@ -608,10 +623,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
             for (int r = 0; r < 4; ++r) {
               const int hh = quad * 16 + (warp >> 2) * 8 + i0 + r;
               if (hh >= nr) continue;
-              // 2^ex2 takes the largest magnitude to [2^14, 2^15)
+              // 2^ex2 takes the largest magnitude to [2^14, 2^15); a row with a NaN or an
+              // infinity is staged as zeros and marked by a negative factor
               int ex2 = 0;
               const uint32_t eb = (amax[r] >> 7) & 0xffu;
-              if (amax[r] != 0u && eb != 0xffu) ex2 = min(100, max(-100, 15 - ((int)eb - 126)));
+              const bool bad = eb == 0xffu;
+              if (amax[r] != 0u && !bad) ex2 = min(126, 15 - ((int)eb - 126));
               const float up =
                   copysignf(__uint_as_float((uint32_t)(127 + ex2) << 23), p.softmax_scale);
               const uint32_t w[8] = {a[r].x, a[r].y, a[r].z, a[r].w,
@@ -619,12 +636,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
               uint32_t f[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                f[k] = pack_half2(__uint_as_float(w[k] << 16) * up,
-                                  __uint_as_float(w[k] & 0xffff0000u) * up);
+                f[k] = bad ? 0u : pack_half2(__uint_as_float(w[k] << 16) * up,
+                                             __uint_as_float(w[k] & 0xffff0000u) * up);
               const uint32_t qr = qsm + hh * 1024;
               sts128(qr + ((lane ^ (hh & 7)) << 4), make_uint4(f[0], f[1], f[2], f[3]));
               sts128(qr + (((32 + lane) ^ (hh & 7)) << 4), make_uint4(f[4], f[5], f[6], f[7]));
-              if (lane == 0) sm.qdown[hh] = __uint_as_float((uint32_t)(127 - ex2) << 23);
+              if (lane == 0)
+                sm.qdown[hh] = bad ? -1.0f : __uint_as_float((uint32_t)(127 - ex2) << 23);
             }
           }
         }
@@ -932,11 +950,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       bar_sync(kBarQ, kNumQ);
       const int r0 = S.blk * kRows;
       const bool real = r0 + h < p.Tq * p.Hq;
-      const float hs = real ? fabsf(p.softmax_scale) * kLog2e * sm.qdown[h] : 0.0f;
+      const float hs = real ? fabsf(p.softmax_scale) * kLog2e * fabsf(sm.qdown[h]) : 0.0f;
       // entries that this row sees from the segment's first on
       const int n_row = (!kListed && real && p.nvalid ? visible(p, S.b, (r0 + h) / p.Hq) : S.n_most) -
                         S.t0 * kT;
       const uint32_t g0 = S.g0, used0 = S.used0, used1 = S.used1;
+      // (the reference is kept as S has it, and logits are the differences times hs: a
+      // product rounded before the difference is off by its own size 2^-24, which is
+      // more than one for logits of 2^24 and above)
       float m_ref = -INFINITY, l = 0.0f;
       bool ok = true;
       for (int t = 0; t < nt; ++t) {
@@ -972,12 +993,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
           }
           float xmax = fmaxf(fmaxf(xm[0], xm[1]), fmaxf(xm[2], xm[3]));
           xmax = fmaxf(xmax, __shfl_xor_sync(0xffffffffu, xmax, 16));
-          if (xmax != -INFINITY) xmax *= hs;
-          const bool raise = xmax > m_ref + kRescaleSlack;
+          const bool raise = m_ref == -INFINITY ? xmax != -INFINITY
+                                                : (xmax - m_ref) * hs > kRescaleSlack;
           if (__any_sync(0xffffffffu, raise)) {
             float alpha = 1.0f;
             if (raise) {
-              if (m_ref != -INFINITY) alpha = fast_exp2(m_ref - xmax);
+              if (m_ref != -INFINITY) alpha = fast_exp2((m_ref - xmax) * hs);
               m_ref = xmax;
               l *= alpha;
             }
@@ -1009,7 +1030,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int j = 8 * k + 2 * i;
-              float x0 = fast_exp2(fmaf(y[j], hs, -mm)), x1 = fast_exp2(fmaf(y[j + 1], hs, -mm));
+              const float2 z = scaled_difference(y[j], y[j + 1], mm, hs);
+              float x0 = fast_exp2(z.x), x1 = fast_exp2(z.y);
               if (!all) {
                 if (!((j < 32 ? m0 >> j : m1 >> (j - 32)) & 1u)) x0 = 0.0f;
                 if (!((j + 1 < 32 ? m0 >> (j + 1) : m1 >> (j + 1 - 32)) & 1u)) x1 = 0.0f;
@@ -1030,8 +1052,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
         }
         bar_arrive(kBarP + buf, kNumP);
       }
-      const float l_tot = l + __shfl_xor_sync(0xffffffffu, l, 16);
-      if (ch == 0) sm.mlf[h] = make_float2(l_tot > 0.0f ? m_ref : -INFINITY, l_tot);
+      float l_tot = l + __shfl_xor_sync(0xffffffffu, l, 16);
+      if (ch == 0) {
+        if (real && sm.qdown[h] < 0.0f && l_tot > 0.0f) l_tot = NAN;     // and it saw something
+        sm.mlf[h] = make_float2(l_tot == 0.0f ? -INFINITY : m_ref * hs, l_tot);
+      }
     }
 
     // -------------------------------------------------------------- output
@@ -1086,7 +1111,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
         const uint32_t row = vs_s + (uint32_t)(h * 2048);
         // over the row sum (a row that saw nothing has sum 0 and zeros in O): the
         // output in bf16, or a partial, a mean of values and so below 2^12, in fp16
-        const float f = ml.y > 0.0f ? 1.0f / ml.y : 0.0f;
+        const float f = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
         uint4* dst = reinterpret_cast<uint4*>(
             slot < 0 ? reinterpret_cast<uint16_t*>(p.out) + (row0 + h) * kD
                      : reinterpret_cast<uint16_t*>(p.ws_o) + ((size_t)slot * kRows + h) * kD);
@@ -1109,7 +1134,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
           if (slot >= 0)
             p.ws_ml[(size_t)slot * kRows + h] = ml;
           else if (p.lse)
-            p.lse[row0 + h] = ml.y > 0.0f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
+            p.lse[row0 + h] = ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
         }
       }
     }
@@ -1190,11 +1215,11 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const Params p, int 
   }
   const size_t row = b * per_seq + r;
   if (kGroups == 1) {
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     reinterpret_cast<uint4*>(p.out + row * kD)[c] =
         make_uint4(pack_bf162(acc[0] * inv, acc[1] * inv), pack_bf162(acc[2] * inv, acc[3] * inv),
                    pack_bf162(acc[4] * inv, acc[5] * inv), pack_bf162(acc[6] * inv, acc[7] * inv));
-    if (p.lse && c == 0) p.lse[row] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    if (p.lse && c == 0) p.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
     return;
   }
   const int lane = threadIdx.x % kLanes;
@@ -1220,11 +1245,11 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const Params p, int 
       o.y = fmaf(f, v.y, o.y);
     }
   }
-  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   reinterpret_cast<uint32_t*>(p.out + row * kD)[blockIdx.x % kParts * (kChannels / 2) + threadIdx.x] =
       pack_bf162(o.x * inv, o.y * inv);
   if (p.lse && blockIdx.x % kParts == 0 && threadIdx.x == 0)
-    p.lse[row] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    p.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 int sm_count_of_device() {

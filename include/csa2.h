@@ -560,6 +560,7 @@ CSA2_API csa2_status csa2_qk_norm_rope(const csa2_norm_rope_args* args, const fp
  *   lse      float  [B][Tq][Hq]     optional, natural log; no entry gives
  *                            out = 0 and lse = -inf
  *   workspace  csa2_paged_attn_workspace_bytes() bytes (K 0 without topk_idx);
+ * A row of q with a NaN or an infinity gives NaN (out and lse) where it sees an entry.
  * A slot outside [0, S) is recorded and has no entries, and neither has a table
  * place that holds no page. Scale bytes of the rows that are read must not be NaN
  * (0x7f, 0xff; no call of this library writes one). Requires pages->D == 512, 1 <= Hq, Tq >= 0,

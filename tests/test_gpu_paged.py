@@ -441,6 +441,40 @@ def test_dense_with_sharp_softmax(scale):
     assert errors() == "OK"
 
 
+@pytest.mark.parametrize("lens,K", [([200, 70], 0), ([9000, 5000], 0), ([300, 300], 100)])
+def test_queries_of_any_magnitude(lens, K):
+    """Logits of 2^100 and of 2^-100: differences, not the logits themselves, are rounded.
+    A NaN or an infinity in a row of q fills that row, if it sees an entry, and no other."""
+    m, g, slots, q = attn_case(2, 2, 16, lens, 16, seed=12)
+    factor = 2.0 ** torch.tensor([0, 100, -100, 20, 40, 0, 0, 0, 64, -130, 26, 0, 10, 80, 100, 5.0])
+    q = (q.float() * factor.cuda()[:, None]).to(torch.bfloat16)
+    clean = q.clone()
+    q[:, :, 5, 77] = float("nan")
+    q[:, :, 6, 500] = float("inf")
+    q[:, :, 7, 0] = -float("inf")
+    nv = np.array([[lens[0], 0], [0, lens[1] - 3]])
+    ids = None
+    if K:
+        r = np.random.RandomState(5)
+        ids = np.stack([[r.permutation(max(K, n))[:K] if n else np.full(K, -1) for n in row]
+                        for row in nv]).astype(np.int64)
+        ids[ids >= nv[:, :, None]] = -1
+    out, lse = csa2.csa2_paged_attn(q, g, 0.05, seq=i32(slots), nvalid=i32(nv),
+                                    topk_idx=None if ids is None else i32(ids))
+    for b, t in ((0, 0), (1, 1)):
+        assert torch.isnan(out[b, t, 5:8]).all() and torch.isnan(lse[b, t, 5:8]).all()
+    # the other rows, and those that see nothing, as without them
+    want, want_lse = csa2.csa2_paged_attn(clean, g, 0.05, seq=i32(slots), nvalid=i32(nv),
+                                          topk_idx=None if ids is None else i32(ids))
+    rest = [h for h in range(16) if not 5 <= h <= 7]
+    assert torch.equal(out[:, :, rest], want[:, :, rest])
+    assert torch.equal(lse[:, :, rest], want_lse[:, :, rest])
+    for b, t in ((0, 1), (1, 0)):
+        assert torch.equal(out[b, t], want[b, t]) and torch.equal(lse[b, t], want_lse[b, t])
+    check_attn(m, slots, clean, want, want_lse, 0.05, nvalid=nv, ids=ids)
+    assert errors() == "OK"
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3])
 def test_scales_that_are_not_positive(scale):
     """Scale 0: the mean of the visible values; a negative one turns the order round."""
