@@ -529,6 +529,8 @@ cudaError_t launch_qk_norm_rope(const csa2_norm_rope_args& a, const fp4_kv_pages
     path = kExchange;
   // rows per CTA: few rows spread over the SMs, one per warp; many share the start and
   // the cosines, up to 64 of them (64 KB of bf16) while the tables and strips stay in 48 KB
+  // and about a wave of CTAs is left (256 tokens of 64 heads: 512 CTAs of 32 rows 9.4 us,
+  // 1024 of 16 rows 11, 2048 of 8 rows 16)
   const long long all = (long long)a.T * a.Hq;
   const long long words = 48 * 1024 / 4 - (path == kStrip ? kWarps * strip_at(a.D) : 0);
   auto tokens_of = [&](int rows) { return a.T > 0 ? (rows - 2 + a.Hq) / a.Hq + 1 : 0; };   // touched at most
@@ -536,7 +538,7 @@ cudaError_t launch_qk_norm_rope(const csa2_norm_rope_args& a, const fp4_kv_pages
   while (p.rows_per_cta > 1 && (long long)tokens_of(p.rows_per_cta) * a.R > words)
     p.rows_per_cta /= 2;
   const int top = a.D >= 512 || a.q_f32 ? 64 : 64 * 512 / a.D;
-  while (p.rows_per_cta < top && all / (2 * p.rows_per_cta) >= 8ll * sms &&
+  while (p.rows_per_cta < top && all / (2 * p.rows_per_cta) >= 3ll * sms &&
          (long long)tokens_of(2 * p.rows_per_cta) * a.R <= words)
     p.rows_per_cta *= 2;
   p.tokens_per_cta = tokens_of(p.rows_per_cta);

@@ -483,7 +483,8 @@ compact_plan_kernel(const fp4_kv_pages pg, CompactPlan plan, int32_t* used) {
 // Warp 0 of each CTA copies pages, in pieces of at most 16 KB, by bulk copies
 // through a ring of shared memory (no page is both read and written: sources lie
 // at U or above, destinations below); the other warps rewrite the tables.
-// Measured on 16384 pages of 18 KB: register copies 5.0 TB/s read and written.
+// Measured on 16384 pages of 18 KB: 5.7 to 5.9 TB/s read and written (104 us with the
+// tables); copies through registers 5.0.
 constexpr int kPieceMax = 16384, kStages = 4;
 constexpr size_t kCopySmem = (size_t)kStages * kPieceMax;
 
