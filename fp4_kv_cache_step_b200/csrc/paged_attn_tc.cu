@@ -45,7 +45,7 @@
 // What bounds it: the tensor core. An instruction of M = 64, K = 16 takes 47 cycles
 // at N = 80 (and at any N up to 96: the least there is) and 129 at N = 256, so a tile
 // costs 32 x 47 + 10 x 129 = 2794 cycles; measured 2865 (ncu: the tensor pipe active
-// 79 % of the kernel on 32 sequences of 16384 to 32768 entries, 64 heads, 138 us).
+// 73 to 79 % of the kernel on 32 sequences of 16384 to 32768 entries, 64 heads, 138 us).
 // M = 64 leaves half of the array idle; 128 rows of O would be all of tensor memory.
 // Larger tiles would cost less per entry (96 entries: 32.3 cycles instead of 35), but
 // two of them leave no room for the rows to come. Shared memory is the next bound:
