@@ -701,3 +701,49 @@ def test_decode_loop():
     resize(m, g, [0, 1, 2, 3], [0, 0, 0, 0])
     same(m, g)
     assert errors() == "OK" and not m.refs.any()
+
+
+# ---------------------------------------------------------------- calls at once
+@pytest.mark.parametrize("D,H,R,begin,inter", [(512, 3, 64, 448, True), (512, 5, 64, 448, False),
+                                               (1024, 1, 1024, 0, False), (128, 40, 30, 97, True)])
+def test_in_place_as_apart(D, H, R, begin, inter):
+    """Runs of rows across tokens: in place gives the bytes that another output gets."""
+    q = bf16(np.random.RandomState(1).standard_normal((997, H, D))).cuda()
+    pos = torch.randint(0, 1 << 20, (997,), dtype=torch.int32, device="cuda")
+    turns = csa2.csa2_rope_turns(R)
+    w = torch.rand(D, device="cuda")
+    want, _ = csa2.csa2_qk_norm_rope(turns, begin, interleaved=inter, q=q, pos=pos, q_weight=w)
+    got, _ = csa2.csa2_qk_norm_rope(turns, begin, interleaved=inter, q=q, pos=pos, q_weight=w, q_out=q)
+    assert got is q and torch.equal(got, want)
+    assert errors() == "OK"
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own outputs: the bytes of calls made alone."""
+    # short pairs (whole to a piece), long ones (cut), and a list
+    cases = [attn_case(40, 2, 64, [3 + 4 * i for i in range(40)], 16, seed=1),
+             attn_case(3, 1, 64, [7000, 20, 12001], 64, seed=2)]
+    ids = torch.randint(0, 20, (3, 1, 500), dtype=torch.int32, device="cuda")
+    turns = csa2.csa2_rope_turns(64)
+    pos = torch.arange(999, dtype=torch.int32, device="cuda")
+    x = bf16(np.random.RandomState(3).standard_normal((999, 8, 512))).cuda()
+    seqs = [i32(c[2]) for c in cases]
+
+    def call(k):
+        if k == 2:
+            return csa2.csa2_paged_attn(cases[1][3], cases[1][1], 0.05, seq=seqs[1], topk_idx=ids)
+        if k == 3:
+            return csa2.csa2_qk_norm_rope(turns, 448, q=x, pos=pos)[:1]
+        return csa2.csa2_paged_attn(cases[k][3], cases[k][1], 0.05, seq=seqs[k])
+
+    alone = [call(k) for k in range(4)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    results = []
+    for i in range(24):
+        with torch.cuda.stream(streams[i % 2]):
+            results.append((i // 2 % 4, call((i // 2) % 4)))
+    torch.cuda.synchronize()
+    for k, got in results:
+        assert all(torch.equal(a, b) for a, b in zip(got, alone[k])), k
+    assert errors() == "OK"
