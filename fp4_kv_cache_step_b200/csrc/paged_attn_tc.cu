@@ -56,6 +56,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "paged_join.h"
 #include "sm100.cuh"
 
 namespace csa2 {
@@ -151,6 +152,7 @@ struct Params {
   __half* ws_o;       // [slot][64][512]: partial outputs, each over its own row sum
   float2* ws_ml;      // [slot][64]
   int4* ws_info;      // [B][nblk]: first and last piece, the first one's slot
+  int pieces;         // of the line of tiles: ws_o and ws_ml have two slots each
   int* err;
 };
 
@@ -1172,7 +1174,8 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const Params p, int 
   const size_t b = (size_t)b0 + blockIdx.y;
   const int4 info = p.ws_info[b * p.nblk + r / kRows];
   const int first = info.x, last = info.y;
-  if (first == last) return;
+  // (nothing is joined of a pair whose CTA gave up before it wrote its record)
+  if (first == last || !join_record_holds(first, last, info.z, p.pieces)) return;
   const int h = r % kRows;
   const int c = blockIdx.x % kParts * kLanes + threadIdx.x % kLanes;   // of 64, 8 channels each
   float M = -INFINITY, L = 0.0f;
@@ -1186,7 +1189,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const Params p, int 
       ml[k] = make_float2(-INFINITY, 0.0f);
       u[k] = make_uint4(0, 0, 0, 0);
       if (i <= last) {
-        const size_t at = (size_t)(i == first ? info.z : 2 * i) * kRows + h;
+        const size_t at = (size_t)join_slot(i, first, info.z) * kRows + h;
         ml[k] = p.ws_ml[at];
         u[k] = *reinterpret_cast<const uint4*>(p.ws_o + at * kD + 8 * c);
       }
@@ -1329,6 +1332,7 @@ cudaError_t launch_paged_attn(const uint16_t* q, const fp4_kv_pages& pg, const i
   p.out = out;
   p.lse = lse;
   const int pieces = sh.pieces();
+  p.pieces = pieces;
   p.share = ((long long)sh.B * sh.nblk + pieces - 1) / pieces;
   unsigned char* w = static_cast<unsigned char*>(workspace);
   p.ws_info = reinterpret_cast<int4*>(w);
