@@ -22,6 +22,12 @@
 // partials with their (maximum, sum), which paged_combine_kernel joins. A sequence
 // without entries has one empty tile.
 //
+// What a piece has of a pair is taken in segments of kMostTiles tiles at most, whose
+// sums are joined in fp32 (the carry). A sum in tensor memory loses about a last place
+// (2^-23) at every step of 16 entries, always towards zero, measured: beside a few
+// entries far above a long tail that was 0.5 % of the output at 2^20 entries, and is
+// 2^-11 at most with 64000. (148 row blocks over 2^20 entries: 20.3 ms with and without.)
+//
 // With lists each query token is a sequence of its own here, its list the entries
 // (a place without an id takes its turn as an entry that is not there).
 //
@@ -34,8 +40,10 @@
 // that the softmax of one tile runs beside S of the next, and a tile is filled again
 // while the other is multiplied. Warps 10-13 run the softmax, a thread having half
 // of one row's entries. The reference maximum is lazy (raised, with O rescaled, only
-// by a logit more than 8 above it in log2 units), so P stays below 2^8 in fp16. All
-// sums are fp32.
+// by a logit more than 8 above it in log2 units). P is 2^7 times the exponential, to use
+// fp16's whole range: below 2^15, with 2^-24 (its least step) 2^-31 of the reference.
+// What rounds to 0 of a segment's entries is then at most 2^-16 of the row sum (without
+// the factor 2^-9). All sums are fp32.
 // Warps hand work to each other through named barriers, which cost tens of cycles
 // where a waiting mbarrier's wake-up beside this shared-memory load cost 500 to
 // 800; what the tensor core or the copy engine signals are mbarriers, every wait
@@ -84,6 +92,8 @@ constexpr uint32_t kHalfLanes = 16u << 16;      // lanes 16-31 of a quadrant
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleSlack = 8.0f;
+constexpr float kLift = 7.0f;              // log2 of the factor in P
+constexpr int kMostTiles = 800;            // tiles of a segment at most
 
 // Named barriers (0 is __syncthreads): who arrives -> who waits; all but the first
 // two once per tile, each role passing all of its own in order, so that none is
@@ -110,6 +120,7 @@ struct __align__(8) Bars {
 // (In shared memory, so that no role holds it in registers through its loop.)
 struct Segment {
   int b, blk, t0, nt;        // nt 0: there is none
+  int carry, more;           // sums of the pair's tiles before are in the carry; tiles are left
   int n_most;                // entries that the sequence's queries see at most
   int tiles;
   int slot;                  // where its partial goes, -1: it is whole
@@ -152,6 +163,8 @@ struct Params {
   __half* ws_o;       // [slot][64][512]: partial outputs, each over its own row sum
   float2* ws_ml;      // [slot][64]
   int4* ws_info;      // [B][nblk]: first and last piece, the first one's slot
+  float* ws_carry;    // [piece][64][512]: sums of the segments before, null where none has more
+  float2* ws_carry_ml;      // [piece][64]: their reference and row sum
   int pieces;         // of the line of tiles: ws_o and ws_ml have two slots each
   int* err;
 };
@@ -328,18 +341,19 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) {
   asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// ((a - m) s, (b - m) s), two values to an instruction
-__device__ __forceinline__ float2 scaled_difference(float a, float b, float m, float s) {
+// ((a - m) s + kLift, (b - m) s + kLift), two values to an instruction
+__device__ __forceinline__ float2 lifted_difference(float a, float b, float m, float s) {
   float2 r;
-  asm("{\n\t.reg .b64 x, y;\n\t"
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
       "mov.b64 x, {%2, %3};\n\t"
       "mov.b64 y, {%4, %4};\n\t"
       "add.rn.f32x2 x, x, y;\n\t"
       "mov.b64 y, {%5, %5};\n\t"
-      "mul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 z, {%6, %6};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\t"
       "mov.b64 {%0, %1}, x;\n\t}"
       : "=f"(r.x), "=f"(r.y)
-      : "f"(a), "f"(b), "f"(-m), "f"(s));
+      : "f"(a), "f"(b), "f"(-m), "f"(s), "f"(kLift));
   return r;
 }
 
@@ -417,7 +431,8 @@ __device__ __noinline__ void next_segment(const Params& p, Smem& sm, int at, int
   s.used1 = prev.used1 + (uint32_t)prev.nt / 2;
   s.b = prev.b;
   s.nt = 0;
-  s.blk = s.t0 = s.n_most = s.tiles = s.slot = 0;
+  s.blk = s.t0 = s.n_most = s.tiles = s.slot = s.more = 0;
+  s.carry = prev.nt > 0 && prev.more;                    // the same pair goes on
   long long pos = sm.pos;
   const long long last_pair = sm.end_pair - 1;
   if (pos < sm.end) {
@@ -431,21 +446,26 @@ __device__ __noinline__ void next_segment(const Params& p, Smem& sm, int at, int
       return;
     }
     const int pieces = (int)min((long long)gridDim.x, sm.total), piece = (int)blockIdx.x;
-    s.n_most = n_most >= 0 ? n_most : entries_of<kListed>(p, s.b, false);
+    s.n_most = s.carry ? prev.n_most : n_most >= 0 ? n_most : entries_of<kListed>(p, s.b, false);
     s.tiles = tiles_of(s.n_most);
     const int units = kSetup + s.tiles;
     s.blk = (int)quotient(pos - sm.base, units);
     const long long first = sm.base + (long long)s.blk * units + kSetup;   // the pair's first tile
     pos = max(pos, first);
     s.t0 = (int)(pos - first);
-    s.nt = (long long)s.b * p.nblk + s.blk > last_pair
-               ? 0 : (int)max(0ll, min((long long)(s.tiles - s.t0), sm.end - pos));
-    if (s.nt > 0) {
+    // the piece's tiles of the pair from here on
+    const int part = (long long)s.b * p.nblk + s.blk > last_pair
+                         ? 0 : (int)max(0ll, min((long long)(s.tiles - s.t0), sm.end - pos));
+    s.nt = p.ws_carry ? min(part, kMostTiles) : part;
+    s.more = part > s.nt;
+    if (s.carry) {
+      s.slot = prev.slot;
+    } else if (s.nt > 0) {
       const int slot = 2 * piece + (prev.nt > 0 ? 1 : 0);
-      s.slot = s.nt == s.tiles ? -1 : slot;
+      s.slot = part == s.tiles ? -1 : slot;
       if (s.t0 == 0)
         p.ws_info[(size_t)s.b * p.nblk + s.blk] =
-            make_int4(piece, s.nt == s.tiles ? piece : piece_of(first + s.tiles - 1, pieces, sm.total),
+            make_int4(piece, part == s.tiles ? piece : piece_of(first + s.tiles - 1, pieces, sm.total),
                       slot, 0);
     }
     sm.pos = s.nt > 0 ? pos + s.nt : sm.end;
@@ -1032,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int j = 8 * k + 2 * i;
-              const float2 z = scaled_difference(y[j], y[j + 1], mm, hs);
+              const float2 z = lifted_difference(y[j], y[j + 1], mm, hs);
               float x0 = fast_exp2(z.x), x1 = fast_exp2(z.y);
               if (!all) {
                 if (!((j < 32 ? m0 >> j : m1 >> (j - 32)) & 1u)) x0 = 0.0f;
@@ -1057,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       float l_tot = l + __shfl_xor_sync(0xffffffffu, l, 16);
       if (ch == 0) {
         if (real && sm.qdown[h] < 0.0f && l_tot > 0.0f) l_tot = NAN;     // and it saw something
-        sm.mlf[h] = make_float2(l_tot == 0.0f ? -INFINITY : m_ref * hs, l_tot);
+        sm.mlf[h] = make_float2(l_tot == 0.0f ? -INFINITY : m_ref * hs - kLift, l_tot);
       }
     }
 
@@ -1107,8 +1127,52 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       const int r0 = S.blk * kRows, slot = S.slot;
       const int nr = min(kRows, p.Tq * p.Hq - r0);
       const size_t row0 = (size_t)S.b * p.Tq * p.Hq + r0;
+      const bool more = S.more != 0;
+      if (S.carry || more) {
+        // O and (maximum, sum) with the carry's: into the carry again, or where the
+        // rows are written from. (A thread meets its own values of each row only.)
+#pragma unroll 1
+        for (int h = warp; h < nr; h += kThreads / 32) {
+          const size_t at = (size_t)blockIdx.x * kRows + h;
+          float2 ml = sm.mlf[h];
+          float w = 1.0f, wc = 0.0f;
+          if (S.carry) {
+            const float2 c = p.ws_carry_ml[at];
+            const float m = fmaxf(ml.x, c.x);
+            w = ml.x == m ? 1.0f : exp2f(ml.x - m);
+            wc = c.x == m ? 1.0f : exp2f(c.x - m);
+            ml = make_float2(m, fmaf(ml.y, w, c.y * wc));
+          }
+          __syncwarp();                              // read by every lane
+          if (lane == 0) {
+            if (more) p.ws_carry_ml[at] = ml;
+            else sm.mlf[h] = ml;
+          }
+          const uint32_t row = vs_s + (uint32_t)(h * 2048);
+#pragma unroll
+          for (int k = 0; k < kD / 128; ++k) {
+            const int c = 32 * k + lane;
+            const uint32_t src = row + ((c ^ (h & 7)) << 4);
+            float4* sum = reinterpret_cast<float4*>(p.ws_carry + at * kD) + c;
+            const uint4 o = lds128(src);
+            float4 v = make_float4(__uint_as_float(o.x), __uint_as_float(o.y),
+                                   __uint_as_float(o.z), __uint_as_float(o.w));
+            if (S.carry) {
+              const float4 u = *sum;
+              v = make_float4(fmaf(v.x, w, u.x * wc), fmaf(v.y, w, u.y * wc),
+                              fmaf(v.z, w, u.z * wc), fmaf(v.w, w, u.w * wc));
+            }
+            if (more)
+              *sum = v;
+            else
+              sts128(src, make_uint4(__float_as_uint(v.x), __float_as_uint(v.y),
+                                     __float_as_uint(v.z), __float_as_uint(v.w)));
+          }
+          __syncwarp();
+        }
+      }
 #pragma unroll 2
-      for (int h = warp; h < nr; h += kThreads / 32) {
+      for (int h = more ? nr : warp; h < nr; h += kThreads / 32) {
         const float2 ml = sm.mlf[h];
         const uint32_t row = vs_s + (uint32_t)(h * 2048);
         // over the row sum (a row that saw nothing has sum 0 and zeros in O): the
@@ -1290,11 +1354,15 @@ struct Shape {
       : B(K ? B_ * Tq : B_), rows(K ? Hq : Tq * Hq), nblk(ceil_div(rows, kRows)),
         most(K ? K : (long long)pg.M * pg.page) {}
   // pieces of the line of tiles: one per SM, never more than there can be units
+  long long units() const { return (kSetup + (most + kT - 1) / kT) * B * nblk; }
   int pieces() const {
-    const long long all = (kSetup + (most + kT - 1) / kT) * B * nblk;
+    const long long all = units();
     const int sms = sm_count_of_device();
     return (int)(all < sms ? all : sms);
   }
+  // whether a piece can have more tiles of a pair than a segment (even pieces have
+  // units() / pieces() at most, and pairs are dealt out whole where they are shorter)
+  bool carries() const { return units() / pieces() + 1 > kMostTiles; }
 };
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -1304,8 +1372,10 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 size_t paged_attn_workspace_bytes(const fp4_kv_pages& pg, int B, int Tq, int Hq, int K) {
   const Shape sh(pg, B, Tq, Hq, K);
   const size_t slots = 2 * (size_t)sh.pieces();
+  const size_t carry = sh.carries() ? slots / 2 * kRows : 0;     // rows
   return up256((size_t)sh.B * sh.nblk * sizeof(int4)) + up256(slots * kRows * sizeof(float2)) +
-         slots * kRows * kD * sizeof(__half);
+         up256(slots * kRows * kD * sizeof(__half)) + up256(carry * sizeof(float2)) +
+         carry * kD * sizeof(float);
 }
 
 cudaError_t launch_paged_attn(const uint16_t* q, const fp4_kv_pages& pg, const int32_t* seq,
@@ -1340,6 +1410,10 @@ cudaError_t launch_paged_attn(const uint16_t* q, const fp4_kv_pages& pg, const i
   p.ws_ml = reinterpret_cast<float2*>(w);
   w += up256(2 * (size_t)pieces * kRows * sizeof(float2));
   p.ws_o = reinterpret_cast<__half*>(w);
+  w += up256(2 * (size_t)pieces * kRows * kD * sizeof(__half));
+  p.ws_carry_ml = sh.carries() ? reinterpret_cast<float2*>(w) : nullptr;
+  w += up256((size_t)pieces * kRows * sizeof(float2));
+  p.ws_carry = sh.carries() ? reinterpret_cast<float*>(w) : nullptr;
   p.err = err;
   cudaError_t e = allow_shared_memory();
   if (e != cudaSuccess) return e;
