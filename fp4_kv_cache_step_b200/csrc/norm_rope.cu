@@ -331,6 +331,92 @@ __device__ __forceinline__ void rotate_row(const csa2_norm_rope_args& a, uint64_
   }
 }
 
+// Whether a row's mean(x^2) + eps lies where fp32 squares may have overflowed, or lost
+// bits below 2^-126 that count (NaN too).
+__device__ __forceinline__ bool far_mean(float mean) {
+  // outside [2^-100, 2^100], as bits
+  return __float_as_uint(mean) - 0x0d800000u > 0x71800000u - 0x0d800000u;
+}
+
+// Such a row from its place in memory to its output: the row (and eps) times a power of
+// two that takes the largest magnitude to [1, 2), or [1, 4) at the top of the range. A
+// row with a NaN or an infinity, or of zeros with eps 0, is computed as it is. (In the
+// loop over ordinary rows the same costs registers: 88 -> 96 us for 4096 tokens of 64
+// heads. So these rows, which that loop has not written, come after it.)
+template <int J, int kPath, bool kWide>
+__device__ __forceinline__ void far_row(const csa2_norm_rope_args& a, const void* src,
+                                        uint16_t* dst, float* strip, const float* cs) {
+  const int lane = threadIdx.x & 31;
+  float x[J][8];
+  uint32_t bits = __float_as_uint(sqrtf(a.eps));       // (a NaN is larger than every number)
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int c0 = (lane + 32 * j) * 8;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[j][k] = 0.0f;
+    if (c0 < a.D) load8(src, kWide, (size_t)c0, x[j]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bits = max(bits, __float_as_uint(fabsf(x[j][k])));
+  }
+  bits = __reduce_max_sync(0xffffffffu, bits);
+  const int e = (int)(bits >> 23) - 127;               // -127: zero or subnormal
+  const float up = e == 128 ? 1.0f
+                            : __uint_as_float((uint32_t)(127 - max(-126, min(e, 126))) << 23);
+  float sum = 0.0f;
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[j][k] *= up;
+      sum = fmaf(x[j][k], x[j][k], sum);
+    }
+  const float f = rsqrtf(warp_sum(sum) / a.D + a.eps * up * up);
+  uint64_t y[J][4];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int c0 = (lane + 32 * j) * 8;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[j][k] *= f;
+      if (a.q_weight != nullptr && c0 < a.D) x[j][k] *= __ldg(a.q_weight + c0 + k);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[j][k] = pack2(x[j][2 * k], x[j][2 * k + 1]);
+  }
+  rotate_row<J, kPath>(a, y, strip, cs);
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int c0 = (lane + 32 * j) * 8;
+    if (c0 >= a.D) continue;
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = unpack2(y[j][k]);
+      o[k] = pack_bf162(v.x, v.y);
+    }
+    *reinterpret_cast<uint4*>(dst + c0) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// The rows of this warp with a bit in `bits`, their places found again. (For wide rows: holding
+// the places through the loop over ordinary rows spills there, 794 tokens of 64 heads of
+// 1024 in halves 78 us instead of 74; for narrower ones finding them again does, 92 and 89.)
+template <int J, int kPath, bool kWide>
+__device__ __forceinline__ void far_rows(const NormRope& p, float* table, uint32_t bits) {
+  const csa2_norm_rope_args& a = p.a;
+  const int warp = (int)(threadIdx.x >> 5);
+  const long long r0 = (long long)(blockIdx.x - p.entry_blocks) * p.rows_per_cta;
+  const int t0 = (int)(r0 / a.Hq);
+  float* strip = table + (size_t)p.tokens_per_cta * a.R + (size_t)warp * strip_at(a.D);
+  for (; bits != 0; bits &= bits - 1) {
+    const long long row = r0 + warp + (__ffs(bits) - 1) * kWarps;
+    const int t = (int)(row / a.Hq), h = (int)(row - (long long)t * a.Hq);
+    const size_t at = (size_t)t * a.q_stride + (size_t)h * a.D;
+    far_row<J, kPath, kWide>(a, static_cast<const char*>(a.q) + at * (kWide ? 4 : 2),
+                             a.q_out + row * a.D, strip, table + (t - t0) * a.R);
+  }
+}
+
 // CTAs [0, entry_blocks) take entries, one per warp (they come first, being the
 // longest chains); the others rows_per_cta (token, head) rows, warp w every 8th from w.
 // 64 registers a thread where they suffice: 32 warps per SM, 2 KB each in flight.
@@ -365,6 +451,9 @@ norm_rope_kernel(const __grid_constant__ NormRope p) {
     entry_row<J, kPath>(p, e, cs + a.R, cs);
     return;
   }
+  __shared__ uint32_t far[kWarps];                     // rows left for the end, a bit each
+  far[warp] = 0;
+  __syncwarp();
   const int Hq = a.Hq;
   const long long r0 = (long long)(blockIdx.x - p.entry_blocks) * p.rows_per_cta;
   const int rows = (int)min((long long)p.rows_per_cta, (long long)a.T * Hq - r0);
@@ -381,8 +470,8 @@ norm_rope_kernel(const __grid_constant__ NormRope p) {
   const char* src = static_cast<const char*>(a.q) + (size_t)t0 * token_bytes + lane * 8 * esz;
   uint16_t* dst = a.q_out + r0 * D + lane * 8;
   // (token, head) of this warp's next row to load and to compute, kWarps rows apart
-  int load_row = warp, load_tok = (h0 + warp) / Hq, load_h = h0 + warp - load_tok * Hq;
-  int tok = load_tok, head = load_h;
+  int load_tok = (h0 + warp) / Hq, load_h = h0 + warp - load_tok * Hq;
+  int tok[kRows];                                      // of the rows in flight
   auto next = [&](int& t, int& h) {
     t += p.step_tok;
     h += p.step_head;
@@ -391,20 +480,21 @@ norm_rope_kernel(const __grid_constant__ NormRope p) {
       ++t;
     }
   };
-  auto load = [&](uint4 (&v)[J][kVecs]) {
+  auto load = [&](uint4 (&v)[J][kVecs], int row) -> int {
+    const int t = load_tok;
     const char* at = src + (size_t)load_tok * token_bytes + (size_t)(load_h * D * esz);
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int k = 0; k < kVecs; ++k)
-        v[j][k] = load_row < rows && (lane + 32 * j) * 8 < D
+        v[j][k] = row < rows && (lane + 32 * j) * 8 < D
                       ? __ldcs(reinterpret_cast<const uint4*>(at + (256 * j + 4 * k) * esz))
                       : make_uint4(0, 0, 0, 0);
-    load_row += kWarps;
     next(load_tok, load_h);
+    return t;
   };
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) load(raw[r]);
+  for (int r = 0; r < kRows; ++r) tok[r] = load(raw[r], warp + r * kWarps);
   uint64_t w[J][4];
   const bool weighted = a.q_norm && a.q_weight != nullptr;
 #pragma unroll
@@ -450,7 +540,9 @@ norm_rope_kernel(const __grid_constant__ NormRope p) {
             y[j][k] = pack2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u));
         }
       }
-      load(raw[r]);
+      const int t = tok[r];
+      tok[r] = load(raw[r], row + kRows * kWarps);
+      bool write = true;
       if (a.q_norm) {
         uint64_t s2 = 0;
 #pragma unroll
@@ -459,17 +551,20 @@ norm_rope_kernel(const __grid_constant__ NormRope p) {
           for (int k = 0; k < 4; ++k) s2 = fma2(y[j][k], y[j][k], s2);
         const float2 s = unpack2(s2);
         // (rsqrtf is within 2 ulp; the divide and the square root cost 40 instructions a row)
-        const float f = rsqrtf(fmaf(warp_sum(s.x + s.y), inv_d, a.eps));
+        const float mean = fmaf(warp_sum(s.x + s.y), inv_d, a.eps);
+        write = !far_mean(mean);
+        if (!write) far[threadIdx.x >> 5] |= 1u << (row / kWarps);   // (each lane the same)
+        const float f = rsqrtf(mean);
         const uint64_t f2 = pack2(f, f);
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
           for (int k = 0; k < 4; ++k) y[j][k] = mul2(mul2(y[j][k], f2), w[j][k]);
       }
-      rotate_row<J, kPath>(a, y, strip, table + tok * a.R);
+      rotate_row<J, kPath>(a, y, strip, table + t * a.R);
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        if ((lane + 32 * j) * 8 >= D) continue;
+        if ((lane + 32 * j) * 8 >= D || !write) continue;
         uint32_t o[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -480,8 +575,21 @@ norm_rope_kernel(const __grid_constant__ NormRope p) {
                make_uint4(o[0], o[1], o[2], o[3]));
       }
       row += kWarps;
-      next(tok, head);
     }
+  }
+  if (!a.q_norm) return;
+  __syncwarp();
+  uint32_t bits = far[threadIdx.x >> 5];
+  if (J > 2) {
+    if (bits != 0) far_rows<J, kPath, kWide>(p, table, bits);
+    return;
+  }
+  for (; bits != 0; bits &= bits - 1) {
+    const int row = warp + (__ffs(bits) - 1) * kWarps;
+    const int t = (h0 + row) / Hq, h = h0 + row - t * Hq;
+    far_row<J, kPath, kWide>(a, src - lane * 8 * esz + (size_t)t * token_bytes +
+                                    (size_t)(h * D * esz),
+                             dst - lane * 8 + (size_t)row * D, strip, table + t * a.R);
   }
 }
 

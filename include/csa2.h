@@ -493,7 +493,8 @@ CSA2_API csa2_status csa2_rope_turns(int R, double base, csa2_rope_scaling scali
  *   entries is turned back this way: q = q_out = out, q_norm = 0). Pair i is
  *   channels (2i, 2i + 1) of the rotary part when `interleaved`, else
  *   (i, i + R/2).
- * Queries (T > 0): computed in fp32, written as bf16.
+ * Queries (T > 0): computed in fp32, written as bf16. Rows of any finite magnitude have
+ * their norm (squares beyond fp32's range are taken of the scaled row).
  *   q         [T][Hq][D]    bf16 (q_f32 0) or float (1); tokens q_stride
  *                           elements apart, the heads of a token contiguous
  *   pos       int32 [T]     positions, in [0, 2^31)
