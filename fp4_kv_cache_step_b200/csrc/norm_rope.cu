@@ -30,6 +30,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+// tables and strips: what a launch may have, without the words of far rows
+constexpr size_t kTableBytes = 48 * 1024 - kWarps * sizeof(uint32_t);
 
 // how channels rotate (kPairs: kInLane where the rotary part is not whole chunks)
 enum : int { kNone = 0, kInLane = 1, kPairs = 2, kExchange = 3, kStrip = 4 };
@@ -636,11 +638,11 @@ cudaError_t launch_qk_norm_rope(const csa2_norm_rope_args& a, const fp4_kv_pages
            a.rot_begin / 256 == (a.rot_begin + a.R - 1) / 256)
     path = kExchange;
   // rows per CTA: few rows spread over the SMs, one per warp; many share the start and
-  // the cosines, up to 64 of them (64 KB of bf16) while the tables and strips stay in 48 KB
+  // the cosines, up to 64 of them (64 KB of bf16) while the tables and strips fit
   // and about a wave of CTAs is left (256 tokens of 64 heads: 512 CTAs of 32 rows 9.4 us,
   // 1024 of 16 rows 11, 2048 of 8 rows 16)
   const long long all = (long long)a.T * a.Hq;
-  const long long words = 48 * 1024 / 4 - (path == kStrip ? kWarps * strip_at(a.D) : 0);
+  const long long words = kTableBytes / 4 - (path == kStrip ? kWarps * strip_at(a.D) : 0);
   auto tokens_of = [&](int rows) { return a.T > 0 ? (rows - 2 + a.Hq) / a.Hq + 1 : 0; };   // touched at most
   p.rows_per_cta = kWarps;
   while (p.rows_per_cta > 1 && (long long)tokens_of(p.rows_per_cta) * a.R > words)
@@ -654,10 +656,11 @@ cudaError_t launch_qk_norm_rope(const csa2_norm_rope_args& a, const fp4_kv_pages
   p.step_tok = a.T > 0 ? kWarps / a.Hq : 0;
   p.step_head = a.T > 0 ? kWarps % a.Hq : 0;
   const long long query_blocks = (all + p.rows_per_cta - 1) / p.rows_per_cta;
-  // entries: as many warps as 48 KB of tables and strips allow (D = R = 1024: three)
+  // entries: as many warps as the tables and strips allow (D = R = 1024: five in the lane,
+  // two through the strip)
   const size_t per_entry =
       (a.R + (path == kExchange || path == kStrip ? strip_at(a.D) : 0)) * sizeof(double);
-  p.entries_per_cta = per_entry * kWarps <= 48 * 1024 ? kWarps : (int)(48 * 1024 / per_entry);
+  p.entries_per_cta = per_entry * kWarps <= kTableBytes ? kWarps : (int)(kTableBytes / per_entry);
   // few entries: a CTA each, as their chains are what a small call waits for
   if (a.E <= sms) p.entries_per_cta = 1;
   p.entry_blocks = ceil_div(a.E, p.entries_per_cta);

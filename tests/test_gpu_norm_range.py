@@ -96,3 +96,34 @@ def test_rows_that_have_no_norm():
             for t, h in ((0, 0), (0, 2), (1, 1), (1, 3), (1, 5)):
                 assert torch.equal(got[t, h], want[t, h])
     csa2.check_device_errors()
+
+
+@pytest.mark.parametrize("D,R,inter,T,E", [(768, 768, True, 8003, 300), (768, 768, True, 20, 1),
+                                           (512, 384, True, 33000, 0), (1024, 1024, True, 5, 200),
+                                           (1024, 1024, False, 5, 200), (512, 512, False, 3000, 149),
+                                           (384, 192, False, 29000, 0)])
+def test_tables_as_large_as_they_get(D, R, inter, T, E):
+    """One head: CTAs of as many tokens, and entries, as shared memory has tables for."""
+    gen = torch.Generator().manual_seed(D + T)
+    x = torch.randn((T, 1, D), generator=gen).to(torch.bfloat16)
+    kv = torch.randn((E, D), generator=gen)
+    turns = csa2.csa2_rope_turns(R)
+    pos = torch.arange(T, dtype=torch.int32)
+    kv_pos = torch.arange(E, dtype=torch.int32)
+    kw = {}
+    if E:
+        g = csa2.Fp4Pages.empty(E // 8 + 1, 8, D, 1, E // 8 + 1)
+        one = torch.zeros(1, dtype=torch.int32, device="cuda")
+        csa2.fp4_kv_pages_resize(g, one, one + E)
+        kw = dict(kv=kv.cuda(), kv_pos=kv_pos.cuda(), pages=g, entry=kv_pos.cuda(),
+                  seq=torch.zeros(E, dtype=torch.int32, device="cuda"),
+                  kv_out=torch.empty((E, D), dtype=torch.bfloat16, device="cuda"))
+    got, stored = csa2.csa2_qk_norm_rope(turns, 0, interleaved=inter, q=x.cuda(), pos=pos.cuda(), **kw)
+    some = list(range(0, T, max(1, T // 40))) + [T - 1]
+    check(got[some], x[some], turns, 0, inter, torch.ones(D), 1e-6, pos[some])
+    if E:
+        fixed = turns.cpu().numpy().view(np.uint64)
+        _, vals = pm.quantise(pm.norm_rope(kv.double().numpy(), kv_pos.numpy(), fixed, 0, inter,
+                                           eps=float(np.float32(1e-6))))
+        np.testing.assert_array_equal(stored.double().cpu().numpy(), vals)
+    csa2.check_device_errors()
