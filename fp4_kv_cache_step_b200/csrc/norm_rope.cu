@@ -20,8 +20,8 @@
 // An entry's group of 16 channels is two neighbouring lanes: one exchange gives its
 // maximum, the codes of a lane are one 32-bit word. Bound: HBM (a few dozen
 // instructions per 16 bytes read and written); at single tokens, the launch. Measured:
-// 4096 tokens of 64 heads of 512 channels (bf16) and 1024 entries, 539 MB, in 88 us,
-// 6.1 TB/s (a plain copy: 6.5).
+// 4096 tokens of 64 heads of 512 channels (bf16) and 1024 entries, 539 MB, in 89 us of
+// device time (6.0 TB/s; a plain copy: 6.5), 95 with the host's part.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -421,7 +421,8 @@ __device__ __forceinline__ void far_rows(const NormRope& p, float* table, uint32
 
 // CTAs [0, entry_blocks) take entries, one per warp (they come first, being the
 // longest chains); the others rows_per_cta (token, head) rows, warp w every 8th from w.
-// 64 registers a thread where they suffice: 32 warps per SM, 2 KB each in flight.
+// 64 registers a thread where they suffice (neighbouring channels of 512 in bf16 spill 8
+// bytes, which costs nothing measurable): 32 warps per SM, 2 KB each in flight.
 // Elsewhere 80 and 24 warps (2000 tokens of 40 heads of 512 rotated in halves: 36 us,
 // with 64 registers 42; neighbouring channels in whole chunks 32 and 33).
 constexpr int min_ctas(int J, int path) { return J > 2 ? 2 : path <= kInLane ? 4 : 3; }

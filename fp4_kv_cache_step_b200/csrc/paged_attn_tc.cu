@@ -53,7 +53,8 @@
 // What bounds it: the tensor core. An instruction of M = 64, K = 16 takes 47 cycles
 // at N = 80 (and at any N up to 96: the least there is) and 129 at N = 256, so a tile
 // costs 32 x 47 + 10 x 129 = 2794 cycles; measured 2865 (ncu: the tensor pipe active
-// 73 to 79 % of the kernel on 32 sequences of 16384 to 32768 entries, 64 heads, 138 us).
+// 72 to 79 % of the kernel on 32 sequences of 16384 to 32768 entries, 64 heads, 138 to
+// 140 us).
 // M = 64 leaves half of the array idle; 128 rows of O would be all of tensor memory.
 // Larger tiles would cost less per entry (96 entries: 32.3 cycles instead of 35), but
 // two of them leave no room for the rows to come. Shared memory is the next bound:
@@ -1176,7 +1177,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
         const float2 ml = sm.mlf[h];
         const uint32_t row = vs_s + (uint32_t)(h * 2048);
         // over the row sum (a row that saw nothing has sum 0 and zeros in O): the
-        // output in bf16, or a partial, a mean of values and so below 2^12, in fp16
+        // output in bf16, or a partial, a mean of values and so below 2^12, in fp16 (half a
+        // step is 2^-11 of it, an eighth of the output's 2^-8, for half of fp32's bytes)
         const float f = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
         uint4* dst = reinterpret_cast<uint4*>(
             slot < 0 ? reinterpret_cast<uint16_t*>(p.out) + (row0 + h) * kD

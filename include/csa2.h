@@ -428,6 +428,8 @@ CSA2_API csa2_status fp4_kv_pages_resize(const fp4_kv_pages* pages, const int32_
  * every source is read as it was before the call (so slots may be permuted),
  * the pages that dst[i] held are given back and those of src[i] are shared. No
  * row is copied: fp4_kv_pages_resize does that when a shared page is grown into.
+ * Only the paged entries are forked: the indexer keys of csa2_index_score are the
+ * caller's, contiguous per slot, and the caller copies them.
  *   src, dst   int32 [n]   a source may be listed often, a destination once
  * A pair with a slot outside [0, S), and every pair of a destination listed
  * twice, is recorded (CSA2_ERR_DEVICE_INDEX) and skipped.
